@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "qcache.cuh"
 
 using namespace gr;
 
@@ -125,6 +126,34 @@ int attn_bwd_impl(int time_bias, int B, int64_t T, const int32_t* seq_offsets,
   a.ws_bytes = ws_bytes;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return use_tc(dtype, dh) ? launch_attn_bwd_tc(a, s) : launch_attn_bwd_simt(a, s);
+}
+
+// The checks and arguments that the quantised cache's write and read share.
+int fill_qcache(QcacheArgs& a, int B, int64_t T, const int32_t* off, const int32_t* len,
+                const void* k, const void* v, int64_t tok_stride, int H, int dh, int dtype,
+                int format, void* cache, int64_t R, const int64_t* rows, int32_t* err) {
+  const int es = elem_size(dtype);
+  if (B < 1 || T < 0 || R < 0 || H < 1 || dh < 1 || !off || !rows || !err || !es ||
+      (format != GENRANK_QCACHE_INT8 && format != GENRANK_QCACHE_INT4))
+    return GENRANK_ERR_INVALID_ARG;
+  if (H > kMaxHeads || dh != kQDh || T >= INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  if (tok_stride < (int64_t)H * dh || (tok_stride * es) % 16) return GENRANK_ERR_INVALID_ARG;
+  if (T > 0 && (!k || !v || (R > 0 && !cache))) return GENRANK_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return GENRANK_ERR_INVALID_ARG;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.T = T;
+  a.off = off;
+  a.len = len;
+  a.rows = rows;
+  a.H = H;
+  a.dtype = dtype;
+  a.format = format;
+  a.cache = (uint8_t*)cache;
+  a.R = R;
+  a.tok_stride = tok_stride;
+  a.err = err;
+  return GENRANK_OK;
 }
 
 }  // namespace
@@ -521,6 +550,101 @@ int genrank_attn_fwd_cached(int B, int64_t C, const int32_t* cand_offsets, int m
   c.ts_hist = ts_hist;
   c.max_cand = max_cand;
   return launch_attn_fwd_cached(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t genrank_qcache_row_bytes(int H, int dh, int format) {
+  if (H < 1 || H > kMaxHeads || dh != kQDh ||
+      (format != GENRANK_QCACHE_INT8 && format != GENRANK_QCACHE_INT4))
+    return 0;
+  return (size_t)qrow(H, format).bytes;
+}
+
+int genrank_qcache_append(int B, int64_t T, const int32_t* src_offsets, const int32_t* src_len,
+                          const void* k, const void* v, int64_t tok_stride, int H, int dh,
+                          int dtype, const int32_t* pos, const int64_t* ts, int format,
+                          void* cache, int64_t R, const int64_t* rows, int32_t* dev_err,
+                          genrank_stream_t stream) {
+  if (T > 0 && (!pos || !ts)) return GENRANK_ERR_INVALID_ARG;
+  QcacheArgs a;
+  const int rc = fill_qcache(a, B, T, src_offsets, src_len, k, v, tok_stride, H, dh, dtype, format,
+                             cache, R, rows, dev_err);
+  if (rc || T == 0) return rc;
+  a.k = k;
+  a.v = v;
+  a.pos = pos;
+  a.ts = ts;
+  return launch_qcache_append(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int genrank_qcache_read(int B, int64_t T, const int32_t* dst_offsets, const int32_t* dst_len,
+                        const void* cache, int64_t R, const int64_t* rows, int H, int dh,
+                        int format, void* k, void* v, int64_t tok_stride, int dtype, int32_t* pos,
+                        int64_t* ts, int32_t* dev_err, genrank_stream_t stream) {
+  QcacheArgs a;
+  const int rc = fill_qcache(a, B, T, dst_offsets, dst_len, k, v, tok_stride, H, dh, dtype, format,
+                             const_cast<void*>(cache), R, rows, dev_err);
+  if (rc || T == 0) return rc;
+  a.k_out = k;
+  a.v_out = v;
+  a.pos_out = pos;
+  a.ts_out = ts;
+  return launch_qcache_read(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t genrank_attn_qcached_workspace_size(int B, int64_t C, int H, int dh, int max_cand,
+                                           int max_len) {
+  if (B < 1 || C < 0 || H < 1 || H > kMaxHeads || dh != kQDh || max_cand < 0 || max_len < 0)
+    return 0;
+  return attn_fwd_qcached_workspace(B, C, H, max_cand, max_len);
+}
+
+int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t* cand_offsets, int max_cand,
+                             const void* q_c, const void* k_c, const void* v_c,
+                             int64_t cand_stride, const void* cache, int64_t R,
+                             const int64_t* rows, const int32_t* cache_len, int max_len,
+                             const int64_t* ts_cand, int format, int H, int dh,
+                             const float* slope_pos, const float* slope_time, float scale,
+                             int dtype, void* o, int64_t o_stride, float* lse, void* ws,
+                             size_t ws_bytes, int32_t* dev_err, genrank_stream_t stream) {
+  if (B < 1 || C < 0 || R < 0 || max_cand < 0 || max_len < 0 || H < 1 || dh < 1 ||
+      !cand_offsets || !rows || !cache_len || !slope_pos || !slope_time || !dev_err ||
+      !(scale > 0.f) || !isfinite(scale))
+    return GENRANK_ERR_INVALID_ARG;
+  const int es = elem_size(dtype);
+  if (!es || (format != GENRANK_QCACHE_INT8 && format != GENRANK_QCACHE_INT4))
+    return GENRANK_ERR_INVALID_ARG;
+  if (H > kMaxHeads || !use_tc(dtype, dh)) return GENRANK_ERR_UNSUPPORTED;
+  if (C >= INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  if (cand_stride < (int64_t)H * dh || o_stride < (int64_t)H * dh || (cand_stride * es) % 16 ||
+      (o_stride * es) % 16)
+    return GENRANK_ERR_INVALID_ARG;
+  if (C > 0 && (!q_c || !k_c || !v_c || !ts_cand || !o)) return GENRANK_ERR_INVALID_ARG;
+  if (!aligned16(q_c) || !aligned16(k_c) || !aligned16(v_c) || !aligned16(o) || !aligned16(cache))
+    return GENRANK_ERR_INVALID_ARG;
+  if (R > 0 && !cache) return GENRANK_ERR_INVALID_ARG;
+  for (int h = 0; h < H; ++h)
+    if (!isfinite(slope_pos[h]) || !isfinite(slope_time[h]) || slope_pos[h] < 0.f ||
+        slope_time[h] < 0.f)
+      return GENRANK_ERR_INVALID_ARG;
+  const size_t need = genrank_attn_qcached_workspace_size(B, C, H, dh, max_cand, max_len);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return GENRANK_ERR_WORKSPACE;
+  if (C == 0 || max_cand == 0) return GENRANK_OK;
+  QcachedAttnArgs c;
+  memset(&c, 0, sizeof(c));
+  fill_attn(c.a, B, C, cand_offsets, nullptr, max_cand, q_c, k_c, v_c, cand_stride, H, dh,
+            nullptr, ts_cand, slope_pos, slope_time, scale, dtype, o_stride, dev_err);
+  c.a.o = o;
+  c.a.lse = lse;
+  c.a.ws = ws;
+  c.a.ws_bytes = ws_bytes;
+  c.cache = (const uint8_t*)cache;
+  c.R = R;
+  c.rows = rows;
+  c.len = cache_len;
+  c.format = format;
+  c.max_cand = max_cand;
+  c.max_len = max_len;
+  return launch_attn_fwd_qcached(c, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t genrank_attn_candidates_workspace_size(int B, int64_t T, int H, int dh, int max_seqlen) {

@@ -183,6 +183,48 @@ struct GatherRowsArgs {
 };
 int launch_gather_rows(const GatherRowsArgs& a, cudaStream_t st);
 
+// Rows between a jagged token array and the quantised history cache: user u's first len[u]
+// rows from off[u] (all of its segment when len is null) <-> cache rows rows[u], rows[u] + 1, ...
+struct QcacheArgs {
+  int B;
+  long long T;
+  const int32_t* off;   // [B+1]
+  const int32_t* len;   // [B] or null
+  const int64_t* rows;  // [B] first cache rows
+  int H;
+  int dtype;   // of the token array's keys and values
+  int format;  // GENRANK_QCACHE_INT8 or GENRANK_QCACHE_INT4
+  uint8_t* cache;
+  long long R;           // rows of the cache
+  long long tok_stride;  // elements
+  const void* k;         // append
+  const void* v;
+  const int32_t* pos;
+  const int64_t* ts;
+  void* k_out;  // read
+  void* v_out;
+  int32_t* pos_out;  // or null
+  int64_t* ts_out;   // or null
+  int32_t* err;
+};
+int launch_qcache_append(const QcacheArgs& a, cudaStream_t st);
+int launch_qcache_read(const QcacheArgs& a, cudaStream_t st);
+
+// Candidates scored against the quantised cache: `a` describes the candidate rows as in
+// CachedAttnArgs; user u's history is cache rows [rows[u], rows[u] + len[u]).
+struct QcachedAttnArgs {
+  AttnArgs a;
+  const uint8_t* cache;
+  long long R;
+  const int64_t* rows;  // [B]
+  const int32_t* len;   // [B]
+  int format;
+  int max_cand;
+  int max_len;
+};
+int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st);
+size_t attn_fwd_qcached_workspace(int B, long long C, int H, int max_cand, int max_len);
+
 int launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t st);
 int launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t st);
 

@@ -1,0 +1,632 @@
+// Candidate attention over the quantised history cache (sm_100a).
+//
+// Candidate c of user u (position n + 1, time t_c) sees the user's n cached rows and itself:
+//   s_cj = scale q_c.k_j - m_h |n + 1 - p_j| - m_t,h |t_c - t_j|,   s_cc = scale q_c.k_c
+// With k_j = s_j c_j (whole codes c_j, one scale a token and head) the score is
+// (q_c.c_j) (s_j scale log2 e) + col_j, where col_j = log2 e (m_h (p_j - n - 1) +
+// m_t,h (t_j - t_0)) is the key's part of the bias against the user's first candidate time t_0
+// and the row's part, log2 e m_t,h (t_c - t_0), cancels in the softmax.  Codes of at most 7 bits
+// are exact in fp16, so q.c has exact products and fp32 sums: no key is ever rounded.
+//
+// One pass over the rows with the running maximum and sum of an online softmax:
+//   * A block takes one user, up to 8 heads (a warp each), up to 32 candidates and a range of
+//     the history.  A row of the cache holds every head's keys and values next to one another,
+//     so 32 rows are one contiguous piece: one more warp copies such tiles into a ring of
+//     shared-memory stages with bulk copies (wider models: a few per row).
+//   * A warp multiplies codes as the 16-row operand of m16n8k16 (keys for S^T = K q^T, head
+//     dimensions for O^T = V^T P^T), candidates in the 8 columns, so that one candidate wastes
+//     7/8 of a column tile and not 15/16 of a row tile; the work per row is the unpacking: three
+//     instructions per code pair, no conversions.  The candidate's P^T operand is S^T's
+//     accumulator transposed 8 x 8 (movmatrix); the key order inside a tile is permuted so that
+//     the shared-memory reads of eight lanes fall into different banks for every row length.
+//   * V's scale is folded into P (p_j s_j, fp16 with a power-of-two range shift): 11 bits where
+//     rounding P or V to bf16 would cost as much again as rounding the output does.
+//   * The maximum moves only when a score passes it by 2^8, and the first one is the
+//     candidate's own score: most tiles take one vote and no shuffles.
+//   * Short of blocks, the history is cut into ranges; the ranges' (max, sum, O) in fp32 are
+//     joined by a second kernel, always in the same order.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "kernels.h"
+#include "qcache.cuh"
+
+namespace gr {
+namespace qca {
+
+constexpr int kRows = 32;    // cache rows of a tile
+constexpr int kHeads = 8;    // heads of a block, one warp each
+constexpr int kMaxStages = 4;
+constexpr int kThreads = (kHeads + 1) * 32;
+constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
+constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
+constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
+constexpr int kPart = kQDh + 2;  // floats of a range's result: O, max, sum
+
+struct Params {
+  QcachedAttnArgs c;
+  int groups;  // of 8 heads
+  int ctiles;  // candidate tiles of a user
+  int splits;  // ranges of the history
+  int chunk;   // rows of a range, a multiple of kRows
+  float* part;  // [splits][C][H][kPart], or null: one range, written in place
+};
+
+struct Work {
+  int u, g, s, ct;
+};
+GR_DEVICE Work work_of(const Params& P, unsigned i) {
+  Work w;
+  w.ct = i % P.ctiles;
+  i /= P.ctiles;
+  w.s = i % P.splits;
+  i /= P.splits;
+  w.g = i % P.groups;
+  w.u = i / P.groups;
+  return w;
+}
+
+// User u's candidates [c0, c0 + m) and cache rows [at, at + n); false when they do not fit the
+// arrays (flagged by the caller).
+GR_DEVICE bool user_of(const QcachedAttnArgs& c, int u, int& c0, int& m, long long& at, int& n) {
+  const int b = c.a.off[u], e = c.a.off[u + 1];
+  n = c.len[u];
+  at = c.rows[u];
+  c0 = b;
+  m = e - b;
+  return b >= 0 && e >= b && e <= c.a.T && n >= 0 && at >= 0 && n <= c.R && at <= c.R - n;
+}
+
+GR_DEVICE void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+GR_DEVICE uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+GR_DEVICE uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+GR_DEVICE uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+GR_DEVICE uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Code pairs as fp16: a field u of a word placed under the exponent of 1024 reads as 1024 + u
+// (16 u when it lies four bits higher), from which one exact subtraction (fused multiply-add)
+// leaves the signed code.
+GR_DEVICE uint32_t low_nibbles(uint32_t w) {  // nibbles 0 and 4
+  return sub_f16((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);  // - 1032
+}
+GR_DEVICE uint32_t high_nibbles(uint32_t w) {  // nibbles 1 and 5: (1024 + 16 u) / 16 - 72
+  return fma_f16((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+GR_DEVICE uint32_t byte_pair(uint32_t w, uint32_t sel) {  // two bytes chosen by sel, - 1152
+  return sub_f16(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
+}
+
+// Key row of a 32-row tile that a lane's index r (0..7) stands for in 16-key half kk: even rows
+// for the accumulator rows 0-7, the next odd one for 8-15.  Any four consecutive r, and the even
+// and the odd r, fall into different bank groups, rows being an odd number of 16 bytes.
+GR_DEVICE int key_row(int r) { return 2 * ((0x57463120u >> (4 * r)) & 7); }
+
+// The 16 head dimensions whose q a lane (t = lane % 4) holds as the B operand, in the order of
+// the codes it reads of a key: k-step ks, slot s (columns 2t.. or 2t+8..), element e.
+template <int FMT>
+GR_DEVICE constexpr int dim_of(int t, int ks, int s, int e) {
+  return FMT == GENRANK_QCACHE_INT4 ? 16 * t + 8 * (ks >> 1) + 2 * (ks & 1) + s + 4 * e
+                                    : 32 * (ks >> 1) + 8 * t + 4 * (ks & 1) + 2 * s + e;
+}
+
+// A key's 16 codes of this lane as the operand's eight registers, [k-step][slot].
+template <int FMT>
+GR_DEVICE void key_codes(const uint8_t* p, int t, uint32_t (&r)[4][2]) {
+  if constexpr (FMT == GENRANK_QCACHE_INT4) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p + 8 * t);
+    const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[2 * i][0] = low_nibbles(ww[i]);
+      r[2 * i][1] = high_nibbles(ww[i]);
+      r[2 * i + 1][0] = low_nibbles(ww[i] >> 8);
+      r[2 * i + 1][1] = high_nibbles(ww[i] >> 8);
+    }
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p + 8 * t);
+    const uint2 b = *reinterpret_cast<const uint2*>(p + 32 + 8 * t);
+    const uint32_t ww[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i][0] = byte_pair(ww[i], 0x4140);
+      r[i][1] = byte_pair(ww[i], 0x4342);
+    }
+  }
+}
+
+// Values 8g..8g+7 of two keys, paired key by key: r[i] = (key a's, key b's) code of 8g + i.
+template <int FMT>
+GR_DEVICE void value_codes(const uint8_t* pa, const uint8_t* pb, int g, uint32_t (&r)[8]) {
+  if constexpr (FMT == GENRANK_QCACHE_INT4) {
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(pa + 4 * g);
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(pb + 4 * g);
+    const uint32_t x = __byte_perm(a, b, 0x5410), y = __byte_perm(a, b, 0x7632);
+    r[0] = low_nibbles(x);
+    r[1] = high_nibbles(x);
+    r[2] = low_nibbles(x >> 8);
+    r[3] = high_nibbles(x >> 8);
+    r[4] = low_nibbles(y);
+    r[5] = high_nibbles(y);
+    r[6] = low_nibbles(y >> 8);
+    r[7] = high_nibbles(y >> 8);
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(pa + 8 * g);
+    const uint2 b = *reinterpret_cast<const uint2*>(pb + 8 * g);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t aa = i ? a.y : a.x, bb = i ? b.y : b.x;
+      const uint32_t lo = __byte_perm(aa, bb, 0x5140), hi = __byte_perm(aa, bb, 0x7362);
+      r[4 * i] = byte_pair(lo, 0x4140);
+      r[4 * i + 1] = byte_pair(lo, 0x4342);
+      r[4 * i + 2] = byte_pair(hi, 0x4140);
+      r[4 * i + 3] = byte_pair(hi, 0x4342);
+    }
+  }
+}
+
+GR_DEVICE float group_max(float x) {  // over the eight lanes of equal lane % 4
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+GR_DEVICE float group_sum(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Params P, int stages) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const QcachedAttnArgs& c = P.c;
+  const AttnArgs& a = c.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Work w = work_of(P, blockIdx.x);
+  int c0, m, n;
+  long long at;
+  if (!user_of(c, w.u, c0, m, at, n)) {
+    if (threadIdx.x == 0) flag(a.err, GENRANK_DERR_LAYOUT);
+    return;
+  }
+  if (threadIdx.x == 0 && (m > c.max_cand || n > c.max_len)) flag(a.err, GENRANK_DERR_LAYOUT);
+  m = min(m, c.max_cand);
+  const int cb = c0 + w.ct * 8 * NT;               // the block's first candidate row
+  const int mt = min(c0 + m - cb, 8 * NT);         // and how many
+  const int lo = w.s * P.chunk, hi = min(min(n, c.max_len), lo + P.chunk);
+  if (mt <= 0 || (w.s > 0 && lo >= hi)) return;
+  const int tiles = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
+  const int heads = min(a.H - w.g * kHeads, kHeads);
+  const QRow L = qrow(a.H, FMT);
+  const QRow S = qrow(min(a.H, kHeads), FMT);  // a row as staged
+  const int stage_bytes = kRows * S.bytes;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], heads);
+    }
+    abort_word = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+
+  if (warp == kHeads) {
+    // ------------------------------------------------------------------ copies
+    const uint8_t* src = c.cache + (at + lo) * (long long)L.bytes;
+    const int scale_bytes = (4 * heads + 15) / 16 * 16;
+    int i = 0;
+    for (; i < tiles; ++i) {
+      const int st = i % stages;
+      const bool ok = i < stages || mbar_wait(&empty[st], (i / stages + 1) & 1, abort_flag, a.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int rows = min(kRows, hi - lo - i * kRows);
+      uint8_t* dst = smem + st * stage_bytes;
+      const uint8_t* from = src + (long long)i * kRows * L.bytes;
+      if (a.H <= kHeads) {
+        if (lane == 0) {
+          mbar_expect_tx(&full[st], rows * L.bytes);
+          bulk_load(dst, from, rows * L.bytes, &full[st]);
+        }
+      } else {
+        if (lane == 0) mbar_expect_tx(&full[st], rows * (2 * heads * L.cb + scale_bytes + 16));
+        __syncwarp();
+        if (lane < rows) {
+          dst += lane * S.bytes;
+          from += (long long)lane * L.bytes;
+          bulk_load(dst, from + w.g * kHeads * L.cb, heads * L.cb, &full[st]);
+          bulk_load(dst + S.scales / 2, from + L.scales / 2 + w.g * kHeads * L.cb, heads * L.cb, &full[st]);
+          bulk_load(dst + S.scales, from + L.scales + w.g * kHeads * 4, scale_bytes, &full[st]);
+          bulk_load(dst + S.tail, from + L.tail, 16, &full[st]);
+        }
+      }
+    }
+    // the copies issued last have landed before the block exits
+    if (lane == 0)
+      for (int x = max(0, i - stages); x < i; ++x) mbar_drain(&full[x % stages], (x / stages) & 1);
+    return;
+  }
+  if (warp >= heads) return;
+
+  // -------------------------------------------------------------------- one head
+  const int h = w.g * kHeads + warp;
+  const int g = lane >> 2, t = lane & 3;
+  const float sp2 = a.slope_pos[h] * kLog2e, st2 = a.slope_time[h] * kLog2e;
+  const float sc2 = a.scale * kLog2e;
+  const long long t_ref = a.ts[c0];
+
+  // q as the B operand (candidate 8 nt + g), scaled by a power of two into fp16's range, and
+  // each candidate's own score
+  uint32_t q[NT][4][2];
+  float self[NT][2];  // of candidates 8 nt + 2t, + 1: the lane's accumulator columns
+  float qs;
+  {
+    float qf[NT][16], own[NT];
+    float amax = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int ci = cb + min(8 * nt + g, mt - 1);
+      const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + ci * a.tok_stride + h * kQDh;
+      const __nv_bfloat16* kr = (const __nv_bfloat16*)a.k + ci * a.tok_stride + h * kQDh;
+      const int d0 = dim_of<FMT>(t, 0, 0, 0), d1 = dim_of<FMT>(t, 2, 0, 0);
+      float kf[16];
+      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d0)), qf[nt]);
+      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d1)), qf[nt] + 8);
+      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d0)), kf);
+      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d1)), kf + 8);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        dot = fmaf(qf[nt][i], kf[i], dot);
+        const float x = fabsf(qf[nt][i]);
+        if (x < INFINITY) amax = fmaxf(amax, x);
+      }
+      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+      own[nt] = dot * sc2;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+    qs = __uint_as_float((uint32_t)(127 + ex) << 23) * sc2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // element of the 16 loaded (two runs of 8 dimensions)
+          const int i0 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 0);
+          const int i1 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 1);
+          q[nt][ks][s] = pack_f16(qf[nt][i0] * down, qf[nt][i1] * down);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) self[nt][e] = __shfl_sync(0xffffffffu, own[nt], 4 * (2 * t + e));
+    }
+  }
+  long long t_min = LLONG_MAX;
+  float row_term[NT][2], mx[NT][2], sum[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long tc = a.ts[cb + min(8 * nt + 2 * t + e, mt - 1)];
+      t_min = min(t_min, tc);
+      row_term[nt][e] = st2 * (float)(tc - t_ref);
+      self[nt][e] += row_term[nt][e];
+      mx[nt][e] = fmaxf(self[nt][e], kLowest);
+      sum[nt][e] = 0.f;
+    }
+  t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, 1));
+  t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, 2));
+
+  float o[4][NT][4];  // dimension 8g + 2i (and + 1: elements 2, 3) of candidates 2t, 2t + 1
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+  float v_top = 0.f, v_down = 0.f;  // power of two >= every V scale so far; 2^kVExp over it
+  bool bad_time = false, bad_pos = false;
+  const int kr0 = key_row(g);                              // this lane's key row (scores)
+  const int va = key_row(2 * t), vb = key_row(2 * t + 1);  // and its pair of value rows
+  bool alive = true;
+
+  for (int i = 0; i < tiles; ++i) {
+    const int st = i % stages;
+    alive = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / stages) & 1, abort_flag, a.err));
+    if (!alive) break;
+    const uint8_t* base = smem + st * stage_bytes;
+    const int rows = hi - lo - i * kRows;  // valid rows of the tile (or more)
+
+    // S^T = K q^T, its scale and bias
+    float s[2][NT][4], vs[2][2];
+    float v_max = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const uint8_t* ra = base + (16 * kk + kr0) * S.bytes;
+      const uint8_t* rb = ra + S.bytes;
+      uint32_t ka[4][2], kb[4][2];
+      key_codes<FMT>(ra + warp * S.cb, t, ka);
+      key_codes<FMT>(rb + warp * S.cb, t, kb);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kk][nt][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t frag[4] = {ka[ks][0], kb[ks][0], ka[ks][1], kb[ks][1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(s[kk][nt], frag, q[nt][ks][0], q[nt][ks][1]);
+      }
+      float ksc[2], col[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint8_t* r = e ? rb : ra;
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(r + S.scales + 4 * warp);
+        const int4 tail = *reinterpret_cast<const int4*>(r + S.tail);
+        const long long tj = (long long)(((uint64_t)(uint32_t)tail.y << 32) | (uint32_t)tail.x);
+        const bool on = 16 * kk + kr0 + e < rows;  // rows past the end hold what the stage held before
+        bad_time |= on && tj > t_min;
+        bad_pos |= on && (tail.z < 0 || tail.z > n + 1);
+        const float dp = (float)min(tail.z - (n + 1), 0);
+        const float dt = (float)min(tj - t_ref, 0ll);
+        ksc[e] = on ? bf16_lo(sc) * qs : 0.f;
+        vs[kk][e] = on ? bf16_hi(sc) : 0.f;
+        col[e] = on ? fmaf(sp2, dp, st2 * dt) : -INFINITY;
+        v_max = fmaxf(v_max, vs[kk][e]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kk][nt][e] = fmaf(s[kk][nt][e], ksc[e >> 1], col[e >> 1]);
+    }
+
+    // the running maxima move (rarely: a score passed one by 2^kSlack, or a V scale is the
+    // largest so far)
+    bool move = v_max > v_top;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+        move |= x > mx[nt][e] + kSlack;
+      }
+    if (__any_sync(0xffffffffu, move)) {
+      float vm = v_max < INFINITY ? v_max : 0.f;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
+      const int ex = max((int)(__float_as_uint(vm) >> 23) - 126, -100);  // 2^ex > vm
+      const float top = fmaxf(v_top, __uint_as_float((uint32_t)(ex + 127) << 23));
+      const float va_ = v_top > 0.f ? v_top / top : 1.f;
+      v_top = top;
+      v_down = (float)(1 << kVExp) / top;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = group_max(
+              fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])));
+          const float next = fmaxf(mx[nt][e], x);
+          const float al = ex2(mx[nt][e] - next);
+          mx[nt][e] = next;
+          sum[nt][e] *= al;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            o[d][nt][e] *= al * va_;
+            o[d][nt][e + 2] *= al * va_;
+          }
+        }
+    }
+
+    // P and O^T += V^T P^T
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t p[NT][2];
+      const float v0 = vs[kk][0] * v_down, v1 = vs[kk][1] * v_down;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e4[e] = ex2(s[kk][nt][e] - mx[nt][e & 1]);
+          sum[nt][e & 1] += e4[e];
+        }
+        p[nt][0] = transpose8x8(pack_f16(e4[0] * v0, e4[1] * v0));
+        p[nt][1] = transpose8x8(pack_f16(e4[2] * v1, e4[3] * v1));
+      }
+      const uint8_t* vp = base + S.scales / 2 + warp * S.cb + 16 * kk * S.bytes;
+      uint32_t fa[8], fb[8];  // even and odd rows: k columns 2t.. and 2t + 8..
+      value_codes<FMT>(vp + va * S.bytes, vp + vb * S.bytes, g, fa);
+      value_codes<FMT>(vp + (va + 1) * S.bytes, vp + (vb + 1) * S.bytes, g, fb);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t frag[4] = {fa[2 * d], fa[2 * d + 1], fb[2 * d], fb[2 * d + 1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(o[d][nt], frag, p[nt][0], p[nt][1]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+  if (!alive) return;
+  if (bad_time && warp == 0) flag(a.err, GENRANK_DERR_TS_ORDER);
+  if (bad_pos && warp == 0) flag(a.err, GENRANK_DERR_POS_RANGE);
+
+  // ---------------------------------------------------------------------- results
+  const float up = v_top * (1.f / (1 << kVExp));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float total = group_sum(sum[nt][e]);
+      const int k = 8 * nt + 2 * t + e;
+      if (k >= mt) continue;
+      const long long ci = cb + k;
+      float x[8];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        x[2 * d] = o[d][nt][e] * up;
+        x[2 * d + 1] = o[d][nt][e + 2] * up;
+      }
+      float l = total;
+      if (w.s == 0) {  // the candidate itself
+        const float ps = ex2(self[nt][e] - mx[nt][e]);
+        float vf[8];
+        Elem<__nv_bfloat16>::unpack(
+            __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.v + ci * a.tok_stride + h * kQDh + 8 * g)), vf);
+        l += ps;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] = fmaf(ps, vf[d], x[d]);
+      }
+      if (P.part) {
+        float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kPart;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) *reinterpret_cast<float2*>(dst + 8 * g + 2 * d) = make_float2(x[2 * d], x[2 * d + 1]);
+        if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(mx[nt][e], l);
+      } else {
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] *= inv;
+        *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + 8 * g) =
+            Elem<__nv_bfloat16>::pack(x);
+        if (a.lse && g == 0) a.lse[(long long)h * a.T + ci] = (mx[nt][e] + log2f(l) - row_term[nt][e]) * kLn2;
+      }
+    }
+}
+
+// Joins the ranges of one user's candidate: a warp per (candidate, head), two dimensions a lane.
+__global__ void __launch_bounds__(kHeads * 32) k_qcached_join(const __grid_constant__ Params P, int nt8) {
+  const AttnArgs& a = P.c.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ct = blockIdx.x % P.ctiles, g = blockIdx.x / P.ctiles % P.groups, u = blockIdx.x / P.ctiles / P.groups;
+  int c0, m, n;
+  long long at;
+  if (!user_of(P.c, u, c0, m, at, n)) return;
+  m = min(m, P.c.max_cand);
+  n = min(n, P.c.max_len);
+  const int h = g * kHeads + warp;
+  if (h >= a.H) return;
+  const int splits = min(P.splits, max(1, (n + P.chunk - 1) / max(1, P.chunk)));
+  const int k1 = min(m, (ct + 1) * nt8);
+  for (int k = ct * nt8; k < k1; ++k) {
+    const long long ci = c0 + k;
+    const float* src = P.part + (ci * a.H + h) * kPart;
+    const long long step = a.T * a.H * kPart;
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 32) top = fmaxf(top, src[s * step + kQDh]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float l = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(src + s * step + kQDh);
+      const float2 v = *reinterpret_cast<const float2*>(src + s * step + 2 * lane);
+      const float f = ex2(ml.x - top);
+      l = fmaf(ml.y, f, l);
+      x0 = fmaf(v.x, f, x0);
+      x1 = fmaf(v.y, f, x1);
+    }
+    const float inv = 1.f / l;
+    reinterpret_cast<uint32_t*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh)[lane] =
+        pack_bf16(x0 * inv, x1 * inv);
+    if (a.lse && lane == 0) {
+      const float rt = a.slope_time[h] * kLog2e * (float)(a.ts[ci] - a.ts[c0]);
+      a.lse[(long long)h * a.T + ci] = (top + log2f(l) - rt) * kLn2;
+    }
+  }
+}
+
+struct Plan {
+  int nt, groups, ctiles, splits, chunk;
+};
+// Blocks are one user's 8 heads and up to 32 candidates; while they do not fill the 148 SMs a few
+// times over, the history is cut into ranges of at least 64 rows.
+Plan plan(int B, int H, int max_cand, int max_len) {
+  Plan p;
+  p.nt = max_cand <= 8 ? 1 : max_cand <= 16 ? 2 : 4;
+  p.groups = (H + kHeads - 1) / kHeads;
+  p.ctiles = (max_cand + 8 * p.nt - 1) / (8 * p.nt);
+  const long long units = (long long)B * p.groups * (p.ctiles > 0 ? p.ctiles : 1);
+  const long long want = (148 * 4 + units - 1) / units;
+  const long long most = (max_len + 63) / 64;
+  const long long s = want < most ? want : most;
+  p.splits = s > 1 ? (int)s : 1;
+  p.chunk = ((max_len + p.splits - 1) / p.splits + kRows - 1) / kRows * kRows;
+  if (p.chunk > 0) p.splits = (max_len + p.chunk - 1) / p.chunk;
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+template <int FMT, int NT>
+int launch(const Params& P, unsigned blocks, cudaStream_t st) {
+  static DeviceOnce once;
+  const QRow S = qrow(P.c.a.H < kHeads ? P.c.a.H : kHeads, FMT);
+  const int stages = FMT == GENRANK_QCACHE_INT4 ? 4 : 3;
+  if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, NT>, kMaxStages * kRows * qrow(kHeads, FMT).bytes))
+    return GENRANK_ERR_CUDA;
+  k_qcached<FMT, NT><<<blocks, kThreads, stages * kRows * S.bytes, st>>>(P, stages);
+  return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
+}
+
+template <int FMT>
+int launch_nt(const Params& P, int nt, unsigned blocks, cudaStream_t st) {
+  return nt == 1 ? launch<FMT, 1>(P, blocks, st) : nt == 2 ? launch<FMT, 2>(P, blocks, st) : launch<FMT, 4>(P, blocks, st);
+}
+
+}  // namespace qca
+
+size_t attn_fwd_qcached_workspace(int B, long long C, int H, int max_cand, int max_len) {
+  const qca::Plan p = qca::plan(B, H, max_cand, max_len);
+  return p.splits > 1 ? (size_t)p.splits * C * H * qca::kPart * sizeof(float) : 0;
+}
+
+int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
+  using namespace qca;
+  const Plan p = plan(c.a.B, c.a.H, c.max_cand, c.max_len);
+  if (p.ctiles == 0) return GENRANK_OK;
+  const long long units = (long long)c.a.B * p.groups * p.ctiles;
+  if (units * p.splits > INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  Params P;
+  P.c = c;
+  P.groups = p.groups;
+  P.ctiles = p.ctiles;
+  P.splits = p.splits;
+  P.chunk = p.chunk;
+  P.part = p.splits > 1 ? (float*)c.a.ws : nullptr;
+  const unsigned blocks = (unsigned)(units * p.splits);
+  const int rc = c.format == GENRANK_QCACHE_INT8 ? launch_nt<GENRANK_QCACHE_INT8>(P, p.nt, blocks, st)
+                                                 : launch_nt<GENRANK_QCACHE_INT4>(P, p.nt, blocks, st);
+  if (rc != GENRANK_OK || p.splits == 1) return rc;
+  k_qcached_join<<<(unsigned)units, kHeads * 32, 0, st>>>(P, 8 * p.nt);
+  return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
+}
+
+}  // namespace gr

@@ -33,8 +33,11 @@ EXPORTS = (
     "genrank_attn_cached_workspace_size", "genrank_attn_fwd_bucketed",
     "genrank_attn_bwd_bucketed", "genrank_attn_fwd_dense_bias", "genrank_linear",
     "genrank_linear_residual_rmsnorm", "genrank_rmsnorm", "genrank_gather_rows",
+    "genrank_qcache_row_bytes", "genrank_qcache_append", "genrank_qcache_read",
+    "genrank_attn_fwd_qcached", "genrank_attn_qcached_workspace_size",
 )
 EPI_STORE, EPI_SILU = 0, 1
+QCACHE_INT8, QCACHE_INT4 = 0, 1
 
 
 class GenRankError(RuntimeError):
@@ -116,6 +119,20 @@ def lib():
             _I, _P, _L, _P, _P, _Z, _P, _P]
         L.genrank_attn_cached_workspace_size.restype = _Z
         L.genrank_attn_cached_workspace_size.argtypes = [_I, _L, _L, _I, _I, _I]
+        L.genrank_qcache_row_bytes.restype = _Z
+        L.genrank_qcache_row_bytes.argtypes = [_I, _I, _I]
+        L.genrank_qcache_append.restype = _I
+        L.genrank_qcache_append.argtypes = [
+            _I, _L, _P, _P, _P, _P, _L, _I, _I, _I, _P, _P, _I, _P, _L, _P, _P, _P]
+        L.genrank_qcache_read.restype = _I
+        L.genrank_qcache_read.argtypes = [
+            _I, _L, _P, _P, _P, _L, _P, _I, _I, _I, _P, _P, _L, _I, _P, _P, _P, _P]
+        L.genrank_attn_fwd_qcached.restype = _I
+        L.genrank_attn_fwd_qcached.argtypes = [
+            _I, _L, _P, _I, _P, _P, _P, _L, _P, _L, _P, _P, _I, _P, _I, _I, _I, _P, _P, _F, _I,
+            _P, _L, _P, _P, _Z, _P, _P]
+        L.genrank_attn_qcached_workspace_size.restype = _Z
+        L.genrank_attn_qcached_workspace_size.argtypes = [_I, _L, _I, _I, _I, _I]
         L.genrank_attn_workspace_size.restype = _Z
         L.genrank_attn_workspace_size.argtypes = [_I, _L, _I, _I, _I, _I]
         _lib = L
@@ -345,6 +362,129 @@ def attn_fwd_cached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, hist_off
         int(o_stride), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         _ptr(dev_err), _stream(stream))
     _check(rc, "genrank_attn_fwd_cached")
+
+
+def _need(what, dev, **tensors):
+    """The quantised cache's tensors: (tensor, dtype, least number of elements, contiguous) by
+    name, all on the CUDA device that the call is made on."""
+    if dev.type != "cuda":
+        raise GenRankError(f"{what}: tensors on {dev}: the library runs on a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        raise GenRankError(f"{what}: tensors on {dev}, but the current device is "
+                           f"cuda:{torch.cuda.current_device()}")
+    for name, (t, dtype, least, contiguous) in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise GenRankError(f"{what}: {name} is on {t.device}, not on {dev}")
+        if t.dtype != dtype:
+            raise GenRankError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+        if t.numel() < least or (contiguous and not t.is_contiguous()):
+            raise GenRankError(f"{what}: {name} must be contiguous with at least {least} elements")
+
+
+def _need_rows(what, name, t, rows, stride, width):
+    """A matrix given by its first element and a row stride stays inside its storage."""
+    if rows > 0 and (t.storage_offset() + (rows - 1) * stride + width) * t.element_size() > \
+            t.untyped_storage().nbytes():
+        raise GenRankError(f"{what}: {name} has fewer than {rows} rows of stride {stride}")
+
+
+def qcache_row_bytes(H, dh, fmt) -> int:
+    """Bytes of one row (one token) of a quantised history cache: allocate it as a uint8 tensor
+    [rows, qcache_row_bytes(H, dh, fmt)].  fmt: QCACHE_INT8 or QCACHE_INT4."""
+    n = int(lib().genrank_qcache_row_bytes(int(H), int(dh), int(fmt)))
+    if n == 0:
+        raise GenRankError(f"qcache: unsupported H={H}, dh={dh} or format {fmt}")
+    return n
+
+
+def _qcache_checks(what, offsets, length, k, v, tok_stride, H, dh, pos, ts, cache, rows, fmt,
+                   dev_err, T):
+    B, dev, rb = rows.numel(), k.device, qcache_row_bytes(H, dh, fmt)
+    if cache.dim() != 2 or cache.shape[1] != rb:
+        raise GenRankError(f"{what}: cache must be uint8 [rows, {rb}]")
+    if v.dtype != k.dtype:
+        raise GenRankError(f"{what}: k and v must share a dtype")
+    _need(what, dev, k=(k, k.dtype, 0, False), v=(v, k.dtype, 0, False),
+          offsets=(offsets, torch.int32, B + 1, True), length=(length, torch.int32, B, True),
+          pos=(pos, torch.int32, T, True), ts=(ts, torch.int64, T, True),
+          cache=(cache, torch.uint8, 0, True), rows=(rows, torch.int64, B, True),
+          dev_err=(dev_err, torch.int32, 1, True))
+    for name, t in (("k", k), ("v", v)):
+        _need_rows(what, name, t, T, tok_stride, H * dh)
+    return B
+
+
+def qcache_append(src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts, cache, rows, fmt,
+                  dev_err, T=None, stream=None):
+    """genrank_qcache_append: rows src_offsets[u] + i (i < src_len[u], or the whole segment with
+    src_len None) of k, v (bf16 or fp32 views, row stride tok_stride), pos and ts become cache
+    rows rows[u] + i.  cache: uint8 [R, qcache_row_bytes(H, dh, fmt)]; rows: int64 [B],
+    ascending; T (default: pos.numel()) rows of the token arrays."""
+    T = pos.numel() if T is None else int(T)
+    B = _qcache_checks("qcache_append", src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts,
+                       cache, rows, fmt, dev_err, T)
+    rc = lib().genrank_qcache_append(
+        B, T, _ptr(src_offsets), _ptr(src_len), _ptr(k), _ptr(v), int(tok_stride), int(H),
+        int(dh), _dtype_code(k), _ptr(pos), _ptr(ts), int(fmt), _ptr(cache),
+        int(cache.shape[0]), _ptr(rows), _ptr(dev_err), _stream(stream))
+    _check(rc, "genrank_qcache_append")
+
+
+def qcache_read(dst_offsets, dst_len, cache, rows, k, v, tok_stride, H, dh, pos, ts, fmt,
+                dev_err, T=None, stream=None):
+    """genrank_qcache_read: cache rows rows[u] + i (i < dst_len[u], or the whole segment) become
+    rows dst_offsets[u] + i of k and v (bf16 or fp32), pos and ts (either may be None).  T
+    (default: k.shape[0]) rows of the outputs."""
+    T = k.shape[0] if T is None else int(T)
+    B = _qcache_checks("qcache_read", dst_offsets, dst_len, k, v, tok_stride, H, dh, pos, ts,
+                       cache, rows, fmt, dev_err, T)
+    rc = lib().genrank_qcache_read(
+        B, T, _ptr(dst_offsets), _ptr(dst_len), _ptr(cache), int(cache.shape[0]), _ptr(rows),
+        int(H), int(dh), int(fmt), _ptr(k), _ptr(v), int(tok_stride), _dtype_code(k),
+        _ptr(pos), _ptr(ts), _ptr(dev_err), _stream(stream))
+    _check(rc, "genrank_qcache_read")
+
+
+def attn_qcached_workspace_size(B, C, H, dh, max_cand, max_len) -> int:
+    return int(lib().genrank_attn_qcached_workspace_size(B, C, H, dh, max_cand, max_len))
+
+
+def attn_fwd_qcached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, cache, rows, cache_len,
+                     max_len, ts_cand, H, dh, slope_pos, slope_time, scale, o, o_stride, lse, ws,
+                     fmt, dev_err, C=None, stream=None):
+    """genrank_attn_fwd_qcached: candidate rows scored against a quantised history cache, user
+    u's history being cache rows [rows[u], rows[u] + cache_len[u]).  The candidate tensors are
+    views whose data_ptr is head 0 of row 0; C defaults to the row count of o; ws may be None
+    when attn_qcached_workspace_size(...) is 0."""
+    what = "attn_fwd_qcached"
+    B = cand_offsets.numel() - 1
+    C = o.shape[0] if C is None else int(C)
+    rb = qcache_row_bytes(H, dh, fmt)
+    if cache.dim() != 2 or cache.shape[1] != rb:
+        raise GenRankError(f"{what}: cache must be uint8 [rows, {rb}]")
+    if len(slope_pos) < H or len(slope_time) < H:
+        raise GenRankError(f"{what}: a slope for each of the {H} heads")
+    dt = q_c.dtype
+    _need(what, q_c.device, q_c=(q_c, dt, 0, False), k_c=(k_c, dt, 0, False),
+          v_c=(v_c, dt, 0, False), o=(o, dt, 0, False),
+          cand_offsets=(cand_offsets, torch.int32, 2, True),
+          cache=(cache, torch.uint8, 0, True), rows=(rows, torch.int64, B, True),
+          cache_len=(cache_len, torch.int32, B, True), ts_cand=(ts_cand, torch.int64, C, True),
+          lse=(lse, torch.float32, H * C, True), ws=(ws, torch.uint8, 0, True),
+          dev_err=(dev_err, torch.int32, 1, True))
+    for name, t in (("q_c", q_c), ("k_c", k_c), ("v_c", v_c)):
+        _need_rows(what, name, t, C, cand_stride, H * dh)
+    _need_rows(what, "o", o, C, o_stride, H * dh)
+    sp, st = _host_floats(slope_pos), _host_floats(slope_time)
+    rc = lib().genrank_attn_fwd_qcached(
+        B, C, _ptr(cand_offsets), int(max_cand), _ptr(q_c), _ptr(k_c), _ptr(v_c),
+        int(cand_stride), _ptr(cache), int(cache.shape[0]), _ptr(rows), _ptr(cache_len),
+        int(max_len), _ptr(ts_cand), int(fmt), int(H), int(dh), ctypes.cast(sp, _P),
+        ctypes.cast(st, _P), float(scale), _dtype_code(q_c), _ptr(o), int(o_stride), _ptr(lse),
+        _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dev_err), _stream(stream))
+    _check(rc, "genrank_attn_fwd_qcached")
 
 
 def attn_fwd_dense_bias(seq_offsets, hist_len, max_seqlen, q, k, v, tok_stride, H, dh, bias,

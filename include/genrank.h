@@ -313,6 +313,95 @@ int genrank_attn_fwd_cached(int B, int64_t C, const int32_t *cand_offsets, int m
 size_t genrank_attn_cached_workspace_size(int B, int64_t C, int64_t Th, int H, int dh,
                                           int max_cand);
 
+/* ---------------------------------------------------------------------------
+ * Quantised history cache.  A server that keeps its users' history keys and values
+ * (huaxiaozhuan "GenRank [2025]" §1.3.2 on the KV cache) holds 4 H dh bytes a token and
+ * layer in bf16, and a request of few candidates is bound by reading them.  These calls
+ * keep them in 8 or 4 bits: genrank_qcache_append writes key/value rows to the cache,
+ * genrank_attn_fwd_qcached scores candidates against it, genrank_qcache_read reads rows
+ * back.  Head dim 64 only.
+ *
+ * Format: one head's 64 keys (or values) of one token are whole codes c_i and one scale s;
+ * the value is c_i s.  With x in bf16 (fp32 inputs are rounded to it first), a = max |x_i|:
+ *   GENRANK_QCACHE_INT8  s = the smallest power of two with a <= 127 s (exponent within
+ *                        [-126, 121]); |c| <= 127
+ *   GENRANK_QCACHE_INT4  s = a / 7 rounded to 5 significant bits, halves up, within
+ *                        [2^-126, 36 * 2^120]; |c| <= 7
+ *   c_i = sign(x_i) floor(|x_i| / s + 1/2), at most that bound
+ * A head with an infinity or a NaN gets the scale NaN, and reads back as NaN.  Every other
+ * value c_i s is exact in bf16: what genrank_qcache_read returns is what
+ * genrank_attn_fwd_qcached computes with, and what genrank_attn_fwd_cached over it would.
+ *
+ * A cache is R rows of genrank_qcache_row_bytes(H, 64, format) bytes, 16-byte aligned, owned
+ * by the caller, a row per token:
+ *   [K codes: H x cb][V codes: H x cb][H x (K scale, V scale) bf16][zeros to 16 bytes]
+ *   [ts int64][pos int32][0 int32][zeros to an odd multiple of 16 bytes]
+ * cb = 64 (int8: one byte c + 128 per value) or 32 (int4: one nibble c + 8 per value, the
+ * low nibble first).  User u's rows are rows[u], rows[u] + 1, ... (a device array), one per
+ * history token, oldest first; the rest of the cache is not read, and never written.
+ * Rows of R or offsets beyond 2^31 bytes are fine. */
+enum { GENRANK_QCACHE_INT8 = 0, GENRANK_QCACHE_INT4 = 1 };
+
+/* Bytes of one cache row (0 for an unsupported H, dh or format): 1072 / 560 at H = 8. */
+size_t genrank_qcache_row_bytes(int H, int dh, int format);
+
+/* Appends key/value rows: for every user u, rows src_offsets[u] + i (i < src_len[u]) of
+ * k, v, pos and ts become cache rows rows[u] + i.  A whole history (src_offsets =
+ * seq_offsets, src_len = hist_len, k and v views of the fused projection) and one new token
+ * of each user (src_offsets = 0..B, src_len = NULL, rows = first row + tokens held) are the
+ * same call.
+ *   src_offsets [B+1] int32 into the T token rows; src_len [B] int32, or NULL for all of a
+ *                user's segment; k, v: [T] rows of H * 64 values in dtype (GENRANK_F32 or
+ *                GENRANK_BF16), row stride tok_stride elements, 16-byte aligned rows
+ *   pos [T] int32 (1-based), ts [T] int64 seconds
+ *   rows [B] int64: ascending, user u's range ending at or before rows[u+1] (users without
+ *                new rows included), so that no two users write one row
+ * A user whose ranges break these rules sets GENRANK_DERR_LAYOUT and is left out. */
+int genrank_qcache_append(int B, int64_t T, const int32_t *src_offsets, const int32_t *src_len,
+                          const void *k, const void *v, int64_t tok_stride, int H, int dh,
+                          int dtype, const int32_t *pos, const int64_t *ts, int format,
+                          void *cache, int64_t R, const int64_t *rows, int32_t *dev_err,
+                          genrank_stream_t stream);
+
+/* Reads cache rows back: for every user u, cache rows rows[u] + i (i < dst_len[u]) become
+ * rows dst_offsets[u] + i of k and v (dtype GENRANK_F32 or GENRANK_BF16, exact in both), pos
+ * and ts (either may be NULL).  Arguments as genrank_qcache_append, the direction reversed;
+ * rows in any order, the same row any number of times.  Other output rows are left alone. */
+int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int32_t *dst_len,
+                        const void *cache, int64_t R, const int64_t *rows, int H, int dh,
+                        int format, void *k, void *v, int64_t tok_stride, int dtype,
+                        int32_t *pos, int64_t *ts, int32_t *dev_err, genrank_stream_t stream);
+
+/* genrank_attn_fwd_cached over the quantised cache: candidate c of user u, at position
+ * n_u + 1 (n_u = cache_len[u]) and time ts_cand[c], against the user's cached rows and itself
+ * (its own key and value unquantised):
+ *   s_cj = scale q_c.k_j - slope_pos[h] |n_u + 1 - pos_j| - slope_time[h] |t_c - ts_j|
+ *   s_cc = scale q_c.k_c;   O_c = sum softmax(s) v;   LSE_c = log sum exp(s)
+ *   B, C, cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, ts_cand, slopes, scale, o,
+ *   o_stride, lse: as genrank_attn_fwd_cached (bf16)
+ *   cache, R, rows [B] int64, cache_len [B] int32: user u's history is cache rows
+ *                [rows[u], rows[u] + cache_len[u]); users in any order, also repeated
+ *   max_len      an upper bound of cache_len[u] (host value)
+ *   ws, ws_bytes at least genrank_attn_qcached_workspace_size(...) bytes (which may be 0:
+ *                then ws may be NULL); contents on entry do not matter
+ * Rows of o and lse beyond cand_offsets[B] are left alone.  Device-detected:
+ * GENRANK_DERR_LAYOUT (a user's offsets or rows outside their arrays: the user is left out;
+ * more than max_cand candidates or max_len rows: the rest is left out), GENRANK_DERR_TS_ORDER
+ * (a cached time after a candidate's), GENRANK_DERR_POS_RANGE (a cached position outside
+ * [0, n_u + 1]); in the last two cases the distance counts as zero. */
+int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t *cand_offsets, int max_cand,
+                             const void *q_c, const void *k_c, const void *v_c,
+                             int64_t cand_stride, const void *cache, int64_t R,
+                             const int64_t *rows, const int32_t *cache_len, int max_len,
+                             const int64_t *ts_cand, int format, int H, int dh,
+                             const float *slope_pos, const float *slope_time, float scale,
+                             int dtype, void *o, int64_t o_stride, float *lse, void *ws,
+                             size_t ws_bytes, int32_t *dev_err, genrank_stream_t stream);
+
+/* Bytes of workspace genrank_attn_fwd_qcached needs for these sizes (0 if none or invalid). */
+size_t genrank_attn_qcached_workspace_size(int B, int64_t C, int H, int dh, int max_cand,
+                                           int max_len);
+
 /* The candidate rows of genrank_attn_fwd only, on its own jagged layout: for every user
  * u the rows [seq_offsets[u] + hist_len[u], seq_offsets[u+1]) of o (and those columns
  * of lse) are written exactly as genrank_attn_fwd defines them; history rows of o and

@@ -13,6 +13,7 @@ from .genrank_oracle import (  # noqa: F401
     attention_fwd_bucketed,
     attention_fwd_cached,
     attention_fwd_dense_bias,
+    attention_fwd_qcached,
     attention_mask,
     bce_loss,
     block_backward,
@@ -21,6 +22,9 @@ from .genrank_oracle import (  # noqa: F401
     embed_assemble_bwd,
     interleaved_layout,
     pair_time_bucket,
+    qcache_quantise,
+    qcache_rows,
+    qcache_values,
     time_bucket,
     token_metadata,
 )

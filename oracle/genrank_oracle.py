@@ -374,6 +374,106 @@ def attention_fwd_cached(q_c, k_c, v_c, cand_offsets, k_hist, v_hist, hist_offse
 
 
 # ----------------------------------------------------------------------------------------
+# the quantised history cache
+# ----------------------------------------------------------------------------------------
+
+def qcache_quantise(x, bits):
+    """Codes (integers) and scales of heads x [..., 64] kept in ``bits`` = 8 or 4.
+
+    x holds bf16 values.  One head has one scale s; with a = max |x|, s is the smallest power
+    of two with a <= 127 s (8 bits; exponent within [-126, 121]) or a / 7 to five significant
+    bits, halves up (4 bits; within [2^-126, 36 * 2^120]); c = sign(x) floor(|x| / s + 1/2),
+    at most 127 or 7.  A head that is not finite has scale NaN and codes 0.
+    """
+    x = np.asarray(x, np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        a = np.abs(x).max(axis=-1)
+        fine = np.isfinite(x).all(axis=-1)
+    a = np.where(fine, a, 0.0)
+    if bits == 8:
+        m, e = np.frexp(a / 127.0)  # a / 127 = m 2^e, m in [1/2, 1)
+        e = np.where(m == 0.5, e - 1, e)
+        s = np.ldexp(1.0, np.clip(np.where(a > 0, e, -126), -126, 121))
+        most = 127.0
+    else:
+        m, e = np.frexp(a / 7.0)
+        s = np.clip(np.ldexp(np.floor(m * 32.0 + 0.5), e - 5), 2.0 ** -126, 36.0 * 2.0 ** 120)
+        most = 7.0
+    z = np.where(fine[..., None], x, 0.0)
+    c = np.sign(z) * np.minimum(np.floor(np.abs(z) / s[..., None] + 0.5), most)
+    return c.astype(np.int64), np.where(fine, s, np.nan)
+
+
+def qcache_rows(k, v, pos, ts, bits):
+    """The cache rows (uint8) of keys and values [N, H, 64] with their positions and times."""
+    N, H = k.shape[:2]
+    cb = 8 * bits
+    scales = 2 * H * cb
+    tail = -(-(scales + 4 * H) // 16) * 16
+    size = tail + 16 if (tail // 16) % 2 == 0 else tail + 32
+    out = np.zeros((N, size), np.uint8)
+    for side, x in enumerate((k, v)):
+        c, s = qcache_quantise(x, bits)
+        u = (c + (128 if bits == 8 else 8)).astype(np.uint8)
+        if bits == 4:
+            u = u[..., 0::2] + 16 * u[..., 1::2]
+        out[:, side * H * cb:(side + 1) * H * cb] = u.reshape(N, H * cb)
+        s16 = (np.where(np.isnan(s), 0.0, s).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+        s16 = np.where(np.isnan(s), np.uint16(0x7FC0), s16)
+        for h in range(H):
+            out[:, scales + 4 * h + 2 * side] = s16[:, h] & 255
+            out[:, scales + 4 * h + 2 * side + 1] = s16[:, h] >> 8
+    out[:, tail:tail + 8] = np.ascontiguousarray(ts, np.int64).view(np.uint8).reshape(N, 8)
+    out[:, tail + 8:tail + 12] = np.ascontiguousarray(pos, np.int32).view(np.uint8).reshape(N, 4)
+    return out
+
+
+def qcache_values(x, bits):
+    """The values [..., 64] that quantised heads x stand for."""
+    c, s = qcache_quantise(x, bits)
+    return c * s[..., None]
+
+
+def attention_fwd_qcached(q_c, k_c, v_c, cand_offsets, k_val, v_val, rows, cache_len, pos, ts,
+                          ts_cand, slope_pos, slope_time, scale):
+    """``attention_fwd_cached`` with user u's history in rows [rows[u], rows[u] + cache_len[u])
+    of the cache's values k_val, v_val [R, H, 64], pos and ts (users in any order), an array
+    operation a user.  Returns O, the natural-log LSE, the weighted magnitude sum_j p_j |v_j|
+    of each output and the largest scale sum_i |q_i k_i| of each row, by which rounding errors
+    are bounded."""
+    q_c, k_c, v_c = (np.asarray(x, np.float64) for x in (q_c, k_c, v_c))
+    C, H, dh = q_c.shape
+    O, A = np.zeros((C, H, dh)), np.zeros((C, H, dh))
+    LSE, S = np.full((H, C), np.nan), np.zeros((H, C))
+    sp = np.asarray(slope_pos, np.float64)[:, None, None]
+    st = np.asarray(slope_time, np.float64)[:, None, None]
+    for u in range(len(cand_offsets) - 1):
+        c0, c1, r0, n = int(cand_offsets[u]), int(cand_offsets[u + 1]), int(rows[u]), int(cache_len[u])
+        if c1 == c0:
+            continue
+        q, k, v = (x[c0:c1].transpose(1, 0, 2) for x in (q_c, k_c, v_c))  # [H, m, dh]
+        K = np.asarray(k_val[r0:r0 + n], np.float64).transpose(1, 0, 2)
+        V = np.asarray(v_val[r0:r0 + n], np.float64).transpose(1, 0, 2)
+        dp = np.abs(n + 1 - np.asarray(pos[r0:r0 + n], np.int64)).astype(np.float64)
+        dt = np.abs(np.asarray(ts_cand[c0:c1], np.int64)[:, None]
+                    - np.asarray(ts[r0:r0 + n], np.int64)[None]).astype(np.float64)
+        s = q @ K.transpose(0, 2, 1) * scale - sp * dp - st * dt
+        own = (q * k).sum(-1)[..., None] * scale
+        x = np.concatenate([s, own], -1)
+        top = x.max(-1, keepdims=True)
+        w = np.exp(x - top)
+        z = w.sum(-1, keepdims=True)
+        p = w / z
+        O[c0:c1] = (p[..., :n] @ V + p[..., n:] * v).transpose(1, 0, 2)
+        A[c0:c1] = (p[..., :n] @ np.abs(V) + p[..., n:] * np.abs(v)).transpose(1, 0, 2)
+        LSE[:, c0:c1] = (top + np.log(z))[..., 0]
+        mag = np.concatenate([np.abs(q) @ np.abs(K).transpose(0, 2, 1),
+                              np.abs(q * k).sum(-1)[..., None]], -1)
+        S[:, c0:c1] = mag.max(-1) * scale
+    return O, LSE, A, S
+
+
+# ----------------------------------------------------------------------------------------
 # comparison: the interleaved layout with a dense N x N relative bias (a NEXT row)
 # ----------------------------------------------------------------------------------------
 

@@ -1,0 +1,629 @@
+"""The quantised history cache on a GPU: rows written to it bit for bit against the oracle,
+rows read back, and candidate attention over it against the float64 oracle on the values the
+cache stands for.
+
+Tolerances.  A cache value is exact, so append and read have none.  Attention, with
+A = sum_j p_j |v_j| and S = max_j scale sum_i |q_i k_i|:
+  O    2^-8 |O| (rounding to bf16) + A (2^-11 (each p_j rounded to fp16) + 2 e) + n 2^-30 max |v|
+       (p_j below fp16's normal range), e the relative error of a p_j:
+  e    2^-18 S (fp32 sums of 64 products and their scale, log2 units) + 2^-19 (the exponential, its
+       argument of at most 2^5 where p_j matters, the sums)
+  LSE  e + 2^-22 (|LSE| + |the row's time term|)
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gen.synth import bf16_round
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def G():
+    from generative_ranking_recommendation_b200 import genrank
+    from generative_ranking_recommendation_b200.csrc import build
+
+    build.build()
+    genrank.lib()
+    return genrank
+
+
+def _dev(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def _fmt(G, bits):
+    return G.QCACHE_INT8 if bits == 8 else G.QCACHE_INT4
+
+
+def _bf16(x):
+    return bf16_round(np.asarray(x, np.float32))
+
+
+def _kv(r, n, H, spread=1.0):
+    """Keys or values [n, H, 64] in bf16: heads of unequal scale."""
+    return _bf16(r.standard_normal((n, H, 64)) * np.exp2(r.uniform(-spread, spread, (n, H, 1))))
+
+
+# ------------------------------------------------------------------------------------------
+# writing
+# ------------------------------------------------------------------------------------------
+
+def _append(G, k, v, pos, ts, off, length, rows, R, bits, dtype=torch.bfloat16, pad=16, cache=None, fill=0x5A):
+    T, H = k.shape[:2]
+    d = H * 64
+    wide = torch.zeros(T, 2 * d + pad, dtype=dtype, device="cuda")
+    wide[:, :d] = _dev(k.reshape(T, d))
+    wide[:, d:2 * d] = _dev(v.reshape(T, d))
+    if cache is None:
+        cache = torch.full((R, G.qcache_row_bytes(H, 64, _fmt(G, bits))), fill, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_append(_dev(off, torch.int32), None if length is None else _dev(length, torch.int32), wide, wide[:, d:],
+                    2 * d + pad, H, 64, _dev(pos, torch.int32), _dev(ts, torch.int64), cache,
+                    _dev(rows, torch.int64), _fmt(G, bits), err)
+    return cache, G.check_error(err)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1, 3, 8, 9, 16, 64])
+def test_append_bytes(G, bits, dtype, H):
+    r = np.random.default_rng(H)
+    seg, length, gap = [3, 0, 40, 1, 17], [2, 0, 33, 1, 17], [0, 2, 1, 0, 3]
+    off = np.concatenate([[0], np.cumsum(seg)])
+    T = int(off[-1]) + 4  # rows of nobody behind the last user
+    shape = (T, H, 64)
+    x = [r.standard_normal(shape) * np.exp2(r.uniform(-20, 20, (T, H, 1))) for _ in range(2)]
+    x = [np.asarray(a, np.float32) for a in x] if dtype == torch.float32 else [_bf16(a) for a in x]
+    pos = r.integers(0, 1000, T)
+    ts = r.integers(-(1 << 40), 1 << 40, T)
+    rows = np.zeros(5, np.int64)
+    at = 1
+    for u in range(5):
+        rows[u] = at + gap[u]
+        at = rows[u] + length[u]
+    R = int(at) + 2
+    cache, code = _append(G, x[0], x[1], pos, ts, off, length, rows, R, bits, dtype)
+    assert code == 0
+    want = np.full((R, cache.shape[1]), 0x5A, np.uint8)
+    for u in range(5):
+        s = slice(int(off[u]), int(off[u]) + length[u])
+        want[rows[u]:rows[u] + length[u]] = oracle.qcache_rows(_bf16(x[0][s]), _bf16(x[1][s]), pos[s], ts[s], bits)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_append_special_heads(G, bits):
+    """Zero heads, the largest and the smallest bf16, halves of a step, every 8-bit mantissa as
+    the maximum, infinities and NaN (whose head alone is lost)."""
+    r = np.random.default_rng(2)
+    k = _kv(r, 300, 2)
+    k[0] = 0.0
+    k[1, 0] = 3.3895313892515355e38
+    k[1, 1] = -3.3895313892515355e38
+    k[2] = 1e-39
+    k[3, 0] = np.arange(64) + 64.5
+    k[3, 1] = (np.arange(64) - 31.5) * 7 / 31.5 * 3
+    k[4, 0, 7] = np.inf
+    k[5, 1, 8] = -np.inf
+    k[6, 0, 9] = np.nan
+    for i in range(128):
+        k[10 + i] = np.exp2(float(i % 7)) * (128 + i) / 128 * (np.arange(128).reshape(2, 64) - 64) / 64
+        k[10 + i, :, 0] = np.exp2(float(i % 7)) * (128 + i) / 128
+    k = _bf16(k)
+    v = k[::-1].copy()
+    n = len(k)
+    pos, ts = np.arange(n), np.arange(n)
+    cache, code = _append(G, k, v, pos, ts, [0, n], None, [0], n, bits)
+    assert code == 0
+    assert np.array_equal(cache.cpu().numpy(), oracle.qcache_rows(k, v, pos, ts, bits))
+
+
+def test_append_layout_errors(G):
+    """Users whose ranges leave the arrays or meet the next user's are left out and flagged."""
+    r = np.random.default_rng(4)
+    k = _kv(r, 12, 1)
+    pos, ts = np.arange(12), np.arange(12)
+
+    def run(off, length, rows, R=40):
+        cache, code = _append(G, k, k, pos, ts, off, length, rows, R, 8)
+        return (cache.cpu().numpy() != 0x5A).any(-1).nonzero()[0].tolist(), code
+
+    ok = [0, 1, 2, 3, 10, 11, 12, 13, 20, 21, 22, 23]
+    assert run([0, 4, 8, 12], None, [0, 10, 20]) == (ok, 0)
+    assert run([0, 4, 8, 12], None, [0, 10, 37]) == (ok[:8], G.DERR["LAYOUT"])       # past the cache
+    assert run([0, 4, 8, 12], None, [-1, 10, 20]) == (ok[4:], G.DERR["LAYOUT"])
+    assert run([0, 4, 8, 12], None, [8, 10, 20]) == (ok[4:], G.DERR["LAYOUT"])       # meets the next user
+    assert run([0, 4, 8, 12], [4, 5, 4], [0, 10, 20]) == (ok[:4] + ok[8:], G.DERR["LAYOUT"])  # longer than its rows
+    assert run([0, 4, 8, 12], [4, -1, 4], [0, 10, 20]) == (ok[:4] + ok[8:], G.DERR["LAYOUT"])
+    assert run([0, 4, 8, 13], None, [0, 10, 20]) == (ok[:8], G.DERR["LAYOUT"])       # past the token rows
+    assert run([0, 4, 4, 8], None, [0, 10, 10]) == (ok[:8], 0)                       # a user without rows
+    assert run([0, 4, 4, 8], None, [0, 3, 10])[1] == G.DERR["LAYOUT"]                # ... in its place all the same
+
+
+def test_rows_beyond_32_bit_offsets(G):
+    """A row whose byte offset passes 2^32, written and read back."""
+    rb = G.qcache_row_bytes(8, 64, G.QCACHE_INT8)
+    R = (1 << 32) // rb + 100
+    r = np.random.default_rng(5)
+    k, v = _kv(r, 3, 8), _kv(r, 3, 8)
+    cache = torch.empty(R, rb, dtype=torch.uint8, device="cuda")
+    cache[0] = 0
+    pos, ts = [5, 6, 7], [1 << 33, 1 << 34, 1 << 35]
+    cache, code = _append(G, k, v, pos, ts, [0, 3], None, [R - 3], R, 8, cache=cache)
+    assert code == 0 and not cache[0].any()
+    assert np.array_equal(cache[R - 3:].cpu().numpy(), oracle.qcache_rows(k, v, pos, ts, 8))
+    out = torch.empty(2, 3, 512, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_read(_dev([0, 3], torch.int32), None, cache, _dev([R - 3], torch.int64), out[0], out[1], 512, 8, 64,
+                  None, None, G.QCACHE_INT8, err)
+    assert G.check_error(err) == 0
+    for side, x in enumerate((k, v)):
+        assert np.array_equal(out[side].float().cpu().numpy().reshape(3, 8, 64), oracle.qcache_values(x, 8))
+    # and scored against
+    q = _bf16(r.standard_normal((1, 3, 8, 64)))
+    o, lse, code = _score(G, q, [0, 1], cache, [R - 3], [3], [1 << 36], 8, 8)
+    assert code & G.DERR["POS_RANGE"]  # positions 5..7 of a history of three
+    cache[R - 3:] = _dev(oracle.qcache_rows(k, v, [1, 2, 3], ts, 8))
+    _compare(G, q, [0, 1], cache, [R - 3], [3], [1 << 36], 8, 8,
+             values=(oracle.qcache_values(k, 8), oracle.qcache_values(v, 8), [1, 2, 3], ts), base=R - 3)
+
+
+# ------------------------------------------------------------------------------------------
+# reading back
+# ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1, 5, 8, 16])
+def test_read_back(G, bits, dtype, H):
+    """Users in any order, one of them twice, some rows only; other output rows left alone."""
+    r = np.random.default_rng(H)
+    N = 60
+    k, v = _kv(r, N, H, 30.0), _kv(r, N, H, 30.0)
+    pos, ts = r.integers(0, 99, N), r.integers(0, 1 << 40, N)
+    cache = _dev(oracle.qcache_rows(k, v, pos, ts, bits))
+    rows, length, seg = [40, 0, 7, 40], [20, 5, 0, 3], [21, 5, 2, 3]
+    off = np.concatenate([[1], 1 + np.cumsum(seg)])
+    T, d = int(off[-1]) + 3, H * 64
+    stride = d + 16
+    out = torch.full((2, T, stride), -7.0, dtype=dtype, device="cuda")
+    po = torch.full((T,), -7, dtype=torch.int32, device="cuda")
+    to = torch.full((T,), -7, dtype=torch.int64, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_read(_dev(off, torch.int32), _dev(length, torch.int32), cache, _dev(rows, torch.int64), out[0], out[1],
+                  stride, H, 64, po, to, _fmt(G, bits), err)
+    assert G.check_error(err) == 0
+    want = np.full((2, T, stride), -7.0)
+    wp, wt = np.full(T, -7), np.full(T, -7)
+    for u in range(4):
+        d0, s = slice(int(off[u]), int(off[u]) + length[u]), slice(rows[u], rows[u] + length[u])
+        want[0, d0, :d] = oracle.qcache_values(k[s], bits).reshape(-1, d)
+        want[1, d0, :d] = oracle.qcache_values(v[s], bits).reshape(-1, d)
+        wp[d0], wt[d0] = pos[s], ts[s]
+    assert np.array_equal(out.double().cpu().numpy(), want)
+    assert np.array_equal(po.cpu().numpy(), wp) and np.array_equal(to.cpu().numpy(), wt)
+
+
+def test_read_layout_errors(G):
+    cache = _dev(oracle.qcache_rows(np.ones((4, 1, 64)), np.ones((4, 1, 64)), range(4), range(4), 4))
+    for rows, off, length in (([3], [0, 2], None), ([-1], [0, 2], None), ([0], [0, 9], None), ([0], [0, 2], [3])):
+        out = torch.full((2, 4, 64), -7.0, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        G.qcache_read(_dev(off, torch.int32), None if length is None else _dev(length, torch.int32), cache,
+                      _dev(rows, torch.int64), out[0], out[1], 64, 1, 64, None, None, G.QCACHE_INT4, err)
+        assert G.check_error(err) == G.DERR["LAYOUT"]
+        assert (out == -7.0).all()
+
+
+# ------------------------------------------------------------------------------------------
+# attention
+# ------------------------------------------------------------------------------------------
+
+def _score(G, qkv, coff, cache, rows, lens, tc, H, bits, slopes=None, poison=True, extra=0, max_cand=None,
+           max_len=None, pad=8, lse=True):
+    """qkv: [3 (q, k, v), C, H, 64] or [C, 3, H, 64] with C = 1; outputs as float64 [C + extra, H, 64], [H, C + extra]."""
+    qkv = np.asarray(qkv)
+    if qkv.shape[0] != 3:
+        qkv = qkv.transpose(1, 0, 2, 3)
+    C, d = qkv.shape[1], H * 64
+    stride = 3 * d + pad
+    x = torch.zeros(C, stride, dtype=torch.bfloat16, device="cuda")
+    for i in range(3):
+        x[:, i * d:(i + 1) * d] = _dev(qkv[i].reshape(C, d))
+    B = len(rows)
+    coff = np.asarray(coff)
+    max_cand = int(np.max(np.diff(coff))) if max_cand is None else max_cand
+    max_len = int(np.max(lens)) if max_len is None else max_len
+    need = G.attn_qcached_workspace_size(B, C + extra, H, 64, max_cand, max_len)
+    ws = torch.full((max(need, 16),), 0xFF if poison else 0, dtype=torch.uint8, device="cuda")
+    o = torch.full((C + extra, d + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ls = torch.full((H, C + extra), float("nan"), dtype=torch.float32, device="cuda") if lse else None
+    if extra:
+        x = torch.cat([x, torch.full((extra, stride), float("nan"), dtype=torch.bfloat16, device="cuda")])
+        tc = list(tc) + [0] * extra
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sp, st = slopes or G.alibi_slopes(H)
+    G.attn_fwd_qcached(_dev(coff, torch.int32), max_cand, x, x[:, d:], x[:, 2 * d:], stride, cache,
+                       _dev(rows, torch.int64), _dev(lens, torch.int32), max_len, _dev(tc, torch.int64), H, 64, sp, st,
+                       0.125, o, d + pad, ls, ws if need else None, _fmt(G, bits), err, C=C + extra)
+    code = G.check_error(err)
+    assert torch.isnan(o[:, d:]).all()  # between the rows' ends and the stride
+    return (o[:, :d].double().cpu().numpy().reshape(C + extra, H, 64),
+            None if ls is None else ls.double().cpu().numpy(), code)
+
+
+def _compare(G, qkv, coff, cache, rows, lens, tc, H, bits, values, base=0, slopes=None, **kw):
+    """values: (k, v, pos, ts) that the cache stands for, from cache row `base` on."""
+    o, lse, code = _score(G, qkv, coff, cache, rows, lens, tc, H, bits, slopes=slopes, **kw)
+    assert code == 0
+    qkv = np.asarray(qkv, np.float64)
+    if qkv.shape[0] != 3:
+        qkv = qkv.transpose(1, 0, 2, 3)
+    sp, st = slopes or G.alibi_slopes(H)
+    k, v, pos, ts = values
+    want, wl, A, S = oracle.attention_fwd_qcached(*qkv, coff, k, v, np.asarray(rows) - base, lens, pos, ts, tc, sp, st, 0.125)
+    C = len(want)
+    extra = len(o) - C
+    assert np.isnan(o[C:]).all() and (lse is None or np.isnan(lse[:, C:]).all())
+    o = o[:C]
+    e = 2.0 ** -18 * S + 2.0 ** -19  # [H, C]
+    n = max(lens) if len(lens) else 0
+    top = max(np.abs(qkv[2]).max(), np.abs(v).max() if len(v) else 0.0)
+    tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -11 + 2 * e.T[:, :, None]) + n * 2.0 ** -30 * top
+    assert np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
+    if lse is not None:
+        row = np.zeros(C)
+        for u in range(len(rows)):
+            c = slice(coff[u], coff[u + 1])
+            if coff[u + 1] > coff[u]:
+                row[c] = np.abs(np.asarray(tc)[c] - np.asarray(tc)[coff[u]])
+        tol = e + 2.0 ** -22 * (np.abs(wl) + np.asarray(st)[:, None] * row)
+        assert np.all(np.abs(lse[:, :C] - wl) <= tol), np.max(np.abs(lse[:, :C] - wl) / tol)
+    return o, lse, extra
+
+
+def _batch(seed, users, H, bits, spread=1.0, tc_spread=0, qscale=1.0, slack=3, order=None):
+    """Users (n, m) with their rows somewhere in a cache whose other rows are noise."""
+    r = np.random.default_rng(seed)
+    B = len(users)
+    lens, cands = [n for n, _ in users], [m for _, m in users]
+    order = r.permutation(B) if order is None else order
+    rows, at = np.zeros(B, np.int64), 2
+    for u in order:
+        rows[u] = at
+        at += lens[u] + int(r.integers(0, slack + 1))
+    R = at + 2
+    k, v = _kv(r, R, H, spread), _kv(r, R, H, spread)
+    pos, ts = np.zeros(R, np.int64), np.zeros(R, np.int64)
+    noise = np.ones(R, bool)
+    for u in range(B):
+        s = slice(rows[u], rows[u] + lens[u])
+        pos[s] = np.arange(1, lens[u] + 1)
+        gaps = np.where(r.random(lens[u]) < 0.5, r.exponential(30.0, lens[u]), r.exponential(3600.0, lens[u]))
+        ts[s] = 1_700_000_000 + np.cumsum(gaps).astype(np.int64)
+        noise[s] = False
+    rb = oracle.qcache_rows(k, v, pos, ts, bits)
+    rb[noise] = r.choice(np.array([0x7F, 0x80, 0xFF, 0xC0], np.uint8), (int(noise.sum()), rb.shape[1]))
+    coff = np.concatenate([[0], np.cumsum(cands)])
+    C = int(coff[-1])
+    qkv = np.stack([_bf16(qscale * r.standard_normal((C, H, 64))), _kv(r, C, H, spread), _kv(r, C, H, spread)])
+    tc = np.zeros(C, np.int64)
+    for u in range(B):
+        last = ts[rows[u] + lens[u] - 1] if lens[u] else 1_700_000_000
+        m = cands[u]
+        tc[coff[u]:coff[u + 1]] = last + 7 + (r.integers(0, tc_spread + 1, m) if tc_spread else 0)
+    values = (oracle.qcache_values(k, bits), oracle.qcache_values(v, bits), pos, ts)
+    return dict(qkv=qkv, coff=coff, cache=rb, rows=rows, lens=lens, tc=tc, H=H, bits=bits), values
+
+
+def _check(G, batch, values, **kw):
+    b = dict(batch)
+    b["cache"] = _dev(b["cache"])
+    return _compare(G, b.pop("qkv"), b.pop("coff"), b.pop("cache"), b.pop("rows"), b.pop("lens"), b.pop("tc"),
+                    b.pop("H"), b.pop("bits"), values, **kw)
+
+
+# (history, candidates): empty histories, users without candidates, lengths around the tile of 32
+# rows, candidates around the tiles of 8, 16 and 32
+SMALL = [(0, 1), (1, 1), (31, 2), (32, 3), (33, 8), (0, 0), (64, 0), (65, 7), (127, 5), (480, 4), (300, 6)]
+MIDDLE = SMALL + [(40, 9), (33, 16), (0, 15)]
+LARGE = MIDDLE + [(100, 31), (63, 32), (96, 33), (5, 70), (480, 129)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("users", [SMALL, MIDDLE, LARGE], ids=["small", "middle", "large"])
+@pytest.mark.parametrize("H", [1, 2, 5, 8, 9, 16])
+def test_attention(G, bits, users, H):
+    _check(G, *_batch(H, users, H, bits, tc_spread=5000), extra=3)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("n,m,H", [(1, 1, 8), (480, 1, 8), (1000, 8, 3), (4097, 1, 8), (2051, 33, 2), (9000, 2, 17),
+                                   (64, 1, 64), (65, 300, 1)])
+def test_one_user_in_ranges(G, bits, n, m, H):
+    """One user: the history is cut into ranges that are joined."""
+    _check(G, *_batch(n, [(n, m)], H, bits))
+
+
+def test_many_users(G):
+    """More blocks than fit at once, 4 and 8 bits, no workspace."""
+    r = np.random.default_rng(9)
+    users = [(int(r.integers(0, 90)), int(r.integers(0, 4))) for _ in range(2000)]
+    batch, values = _batch(9, users, 2, 4)
+    assert G.attn_qcached_workspace_size(2000, len(batch["tc"]), 2, 64, 3, 89) == 0
+    _check(G, batch, values)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_unequal_magnitudes(G, bits):
+    """V scales over 2^+-20 within a history, and scores of some hundreds: the running maximum
+    and the range of P move often; a candidate's own score far above and far below the rest."""
+    batch, values = _batch(11, [(200, 8), (333, 5), (70, 3)], 4, bits, spread=20.0, qscale=1e-4)
+    _check(G, batch, values)
+    batch, values = _batch(12, [(200, 8), (333, 20), (70, 3)], 4, bits, qscale=60.0)
+    batch["qkv"][1, ::3] *= 8.0
+    batch["qkv"][1, 1::3] *= -8.0
+    _check(G, batch, values)
+
+
+def test_extreme_magnitudes_of_q(G):
+    """q of 2^100 against keys of 2^-100, and the other way round; a zero q; candidates of one
+    tile a factor 2^12 apart."""
+    for up in (100, -100):
+        batch, _ = _batch(13, [(77, 4)], 2, 4)
+        r = np.random.default_rng(1)
+        n, R = 77, len(batch["cache"])
+        k, v = _kv(r, R, 2) * np.float32(2.0 ** -up), _kv(r, R, 2)
+        pos, ts = np.zeros(R, np.int64), np.zeros(R, np.int64)
+        s = slice(batch["rows"][0], batch["rows"][0] + n)
+        pos[s], ts[s] = np.arange(1, n + 1), batch["tc"][0] - 5
+        batch["cache"] = oracle.qcache_rows(k, v, pos, ts, 4)
+        batch["qkv"][0] *= np.float32(2.0 ** up)
+        batch["qkv"][0, 1] = 0.0
+        batch["qkv"][0, 2] *= np.float32(2.0 ** -12)
+        batch["qkv"][1] *= np.float32(2.0 ** -up)
+        _check(G, batch, (oracle.qcache_values(k, 4), oracle.qcache_values(v, 4), pos, ts))
+
+
+@pytest.mark.parametrize("slopes", ["none", "position", "time"])
+def test_slopes(G, slopes):
+    H = 3
+    sp = [0.0] * H if slopes != "position" else [2.0, 0.01, 0.0]
+    st = [0.0] * H if slopes != "time" else [1.0, 1e-5, 1e-9]
+    batch, values = _batch(14, [(150, 6), (31, 2), (0, 1)], H, 8, tc_spread=100000)
+    _check(G, batch, values, slopes=(sp, st))
+
+
+def test_far_times(G):
+    """Gaps of centuries between the interactions and the request."""
+    batch, values = _batch(15, [(60, 3)], 2, 4)
+    values[3][values[3] > 0] -= 1 << 33
+    k, v, pos, ts = values
+    batch["cache"] = oracle.qcache_rows(k, v, pos, ts, 4)
+    _check(G, batch, values, slopes=([0.1, 0.0], [1e-9, 1e-10]))
+
+
+def test_repeated_users(G):
+    """The same user twice in a batch, and two users whose rows overlap (a shared prefix)."""
+    batch, values = _batch(16, [(100, 3), (50, 2)], 8, 4, slack=0, order=[0, 1])
+    for k in ("rows", "lens"):
+        batch[k] = list(batch[k])
+    batch["rows"] = [batch["rows"][0], batch["rows"][0], batch["rows"][0]]
+    batch["lens"] = [100, 100, 40]
+    batch["coff"] = np.array([0, 2, 4, 5])
+    batch["tc"][:] = batch["tc"].max()
+    o, _, _ = _check(G, batch, values)
+    batch["qkv"][:, 2:4] = batch["qkv"][:, 0:2]
+    o, _, _ = _check(G, batch, values)
+    assert np.array_equal(o[0:2], o[2:4])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_nan_and_infinity_stay_in_their_rows(G, bits):
+    """A NaN head in a visible row makes that head's outputs NaN for that user's candidates; a
+    NaN or infinite candidate only its own; rows of nobody reach nothing (see _batch's noise)."""
+    users = [(40, 9), (40, 9)]
+    batch, values = _batch(17, users, 4, bits)
+    clean, _, _ = _score(G, batch["qkv"], batch["coff"], _dev(batch["cache"]), batch["rows"], batch["lens"], batch["tc"], 4, bits)
+    for side in (0, 1):
+        k, v, pos, ts = (x.copy() for x in values)
+        (k if side == 0 else v)[batch["rows"][0] + 5, 1, 3] = np.inf
+        rb = batch["cache"].copy()
+        at = batch["rows"][0] + 5
+        rb[at] = oracle.qcache_rows(k[at:at + 1], v[at:at + 1], pos[at:at + 1], ts[at:at + 1], bits)
+        o, lse, code = _score(G, batch["qkv"], batch["coff"], _dev(rb), batch["rows"], batch["lens"], batch["tc"], 4, bits)
+        assert code == 0
+        assert np.isnan(o[:9, 1]).all() and np.array_equal(np.isnan(lse[:, :9]).any(1), [False, side == 0, False, False])
+        keep = np.ones(o.shape[:2], bool)
+        keep[:9, 1] = False
+        assert np.array_equal(o[keep], clean[keep])
+    qkv = batch["qkv"].copy()
+    qkv[0, 2, 0, 5] = np.nan
+    qkv[1, 4, 1, 6] = np.nan
+    qkv[2, 6, 2, 7] = np.nan
+    qkv[0, 8, 3, 7] = np.inf
+    o, lse, code = _score(G, qkv, batch["coff"], _dev(batch["cache"]), batch["rows"], batch["lens"], batch["tc"], 4, bits)
+    assert np.isnan(o[2, 0]).all() and np.isnan(o[4, 1]).all() and np.isnan(o[8, 3]).all()
+    assert np.isnan(o[6, 2, 7]) and np.isnan(lse[:, 6]).sum() == 0
+    keep = np.ones(o.shape[:2], bool)
+    keep[[2, 4, 6, 8], [0, 1, 2, 3]] = False
+    assert np.array_equal(o[keep], clean[keep])
+
+
+def test_attention_layout_and_order_errors(G):
+    batch, values = _batch(18, [(40, 2), (33, 3), (20, 2)], 2, 4, order=[0, 1, 2])
+    b = {k: (list(v) if k in ("rows", "lens") else v) for k, v in batch.items()}
+    cache = _dev(b["cache"])
+    R = len(b["cache"])
+
+    def run(**kw):
+        a = {**b, **kw}
+        return _score(G, a["qkv"], a["coff"], cache, a["rows"], a["lens"], a["tc"], 2, 4,
+                      max_cand=a.get("max_cand"), max_len=a.get("max_len"))
+
+    clean, _, code = run()
+    assert code == 0
+    left = np.ones(7, bool)
+    left[2:5] = False
+    for kw in (dict(rows=[b["rows"][0], R - 5, b["rows"][2]]), dict(rows=[b["rows"][0], -1, b["rows"][2]]),
+               dict(lens=[40, -1, 20])):
+        o, lse, code = run(**kw)
+        assert code == G.DERR["LAYOUT"]
+        assert np.isnan(o[2:5]).all() and np.array_equal(o[left], clean[left])
+    o, _, code = run(max_cand=2)  # the third candidate of the second user is left out
+    assert code == G.DERR["LAYOUT"] and np.isnan(o[4]).all() and np.array_equal(np.delete(o, 4, 0), np.delete(clean, 4, 0))
+    assert run(max_len=39)[2] == G.DERR["LAYOUT"]
+    assert run(coff=np.array([0, 2, 5, 9]))[2] == G.DERR["LAYOUT"]
+    tc = b["tc"].copy()
+    tc[3] -= 1 << 30
+    o, _, code = run(tc=tc)
+    assert code == G.DERR["TS_ORDER"] and np.array_equal(o[:2], clean[:2])
+
+
+def test_equal_to_cached_attention_over_the_read_back(G):
+    """What the quantised attention gives is genrank_attn_fwd_cached over the rows read back, to
+    the rounding of that kernel's bf16 softmax weights (2^-8 of each, and of the output)."""
+    H, bits = 8, 4
+    batch, values = _batch(19, [(480, 40), (17, 3), (0, 2), (129, 20)], H, bits, slack=0, order=[0, 1, 2, 3])
+    o, lse, code = _score(G, batch["qkv"], batch["coff"], _dev(batch["cache"]), batch["rows"], batch["lens"], batch["tc"], H, bits)
+    assert code == 0
+    d, C, Th = H * 64, len(batch["tc"]), sum(batch["lens"])
+    hoff = _dev(np.concatenate([[0], np.cumsum(batch["lens"])]), torch.int32)
+    kv = torch.empty(Th, 2 * d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.empty(Th, dtype=torch.int32, device="cuda")
+    ts = torch.empty(Th, dtype=torch.int64, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_read(hoff, None, _dev(batch["cache"]), _dev(batch["rows"], torch.int64), kv, kv[:, d:], 2 * d, H, 64, pos, ts,
+                  G.QCACHE_INT4, err)
+    x = _dev(batch["qkv"].transpose(1, 0, 2, 3).reshape(C, 3 * d), torch.bfloat16)
+    ws = torch.empty(G.attn_cached_workspace_size(4, C, Th, H, 64, 40), dtype=torch.uint8, device="cuda")
+    oc = torch.empty(C, d, dtype=torch.bfloat16, device="cuda")
+    lc = torch.empty(H, C, dtype=torch.float32, device="cuda")
+    sp, st = G.alibi_slopes(H)
+    G.attn_fwd_cached(_dev(batch["coff"], torch.int32), 40, x, x[:, d:], x[:, 2 * d:], 3 * d, hoff, kv, kv[:, d:], 2 * d,
+                      pos, ts, _dev(batch["tc"], torch.int64), H, 64, sp, st, 0.125, oc, d, lc, ws, err, C=C, Th=Th)
+    assert G.check_error(err) == 0
+    qkv = batch["qkv"].astype(np.float64)
+    _, _, A, _ = oracle.attention_fwd_qcached(*qkv, batch["coff"], values[0], values[1], batch["rows"], batch["lens"],
+                                              values[2], values[3], batch["tc"], sp, st, 0.125)
+    oc = oc.double().cpu().numpy().reshape(C, H, 64)
+    assert np.all(np.abs(o - oc) <= 2.0 ** -7 * np.abs(oc) + 2.0 ** -7 * A)
+    assert np.max(np.abs(lse - lc.double().cpu().numpy())) <= 1e-3
+
+
+# ------------------------------------------------------------------------------------------
+# together, and under streams and graphs
+# ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_a_server_s_run(G, bits):
+    """Histories written from a fused projection, tokens appended one at a time, scored after
+    each: as if every key and value had been quantised at once."""
+    r = np.random.default_rng(21)
+    B, H, m, room = 5, 8, 3, 50
+    d, fmt = H * 64, _fmt(G, bits)
+    n = np.array([0, 3, 31, 32, 40])
+    k, v = _kv(r, B * room, H).reshape(B, room, H, 64), _kv(r, B * room, H).reshape(B, room, H, 64)
+    ts = 1_700_000_000 + np.cumsum(r.integers(0, 900, (B, room)), 1)
+    first = np.arange(B) * room
+    cache = torch.full((B * room, G.qcache_row_bytes(H, 64, fmt)), 0xFF, dtype=torch.uint8, device="cuda")
+    # the fused projection of the scoring layout: each user's history, then its candidates
+    seq = np.concatenate([[0], np.cumsum(n + m)])
+    qkv = torch.zeros(int(seq[-1]), 3 * d, dtype=torch.bfloat16, device="cuda")
+    pos0, ts0 = np.zeros(int(seq[-1])), np.zeros(int(seq[-1]))
+    for u in range(B):
+        s = slice(int(seq[u]), int(seq[u]) + int(n[u]))
+        qkv[s, d:2 * d] = _dev(k[u, :n[u]].reshape(-1, d))
+        qkv[s, 2 * d:] = _dev(v[u, :n[u]].reshape(-1, d))
+        pos0[s], ts0[s] = np.arange(1, n[u] + 1), ts[u, :n[u]]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_append(_dev(seq, torch.int32), _dev(n, torch.int32), qkv[:, d:], qkv[:, 2 * d:], 3 * d, H, 64,
+                    _dev(pos0, torch.int32), _dev(ts0, torch.int64), cache, _dev(first, torch.int64), fmt, err)
+    values = (oracle.qcache_values(k.reshape(-1, H, 64), bits), oracle.qcache_values(v.reshape(-1, H, 64), bits),
+              np.tile(np.arange(1, room + 1), B), ts.reshape(-1))
+    one = _dev(np.arange(B + 1), torch.int32)
+    for step in range(4):
+        at = np.arange(B), n
+        G.qcache_append(one, None, _dev(k[at].reshape(B, d), torch.bfloat16), _dev(v[at].reshape(B, d), torch.bfloat16), d,
+                        H, 64, _dev(n + 1, torch.int32), _dev(ts[at], torch.int64), cache, _dev(first + n, torch.int64), fmt, err)
+        n = n + 1
+        q = np.stack([_bf16(r.standard_normal((B * m, H, 64))) for _ in range(3)])
+        tc = np.repeat(ts[np.arange(B), n - 1] + 60, m)
+        _compare(G, q, np.arange(B + 1) * m, cache, first, n.tolist(), tc, H, bits, values)
+    assert G.check_error(err) == 0
+    untouched = np.concatenate([np.arange(first[u] + n[u], first[u] + room) for u in range(B)])
+    assert (cache[_dev(untouched)] == 0xFF).all()
+
+
+def test_streams_and_graphs(G):
+    """Calls on a side stream; two captured graphs (a joined and a direct one) replayed in turn on
+    changed inputs, bit for bit the eager results."""
+    cases = [_batch(22, [(700, 2)], 8, 4), _batch(23, [(50, 3)] * 200, 8, 8)]
+    H, d, fmts = 8, 512, [G.QCACHE_INT4, G.QCACHE_INT8]
+    sp, st = G.alibi_slopes(H)
+    calls = []
+    for (b, _), fmt in zip(cases, fmts):
+        C = len(b["tc"])
+        x = _dev(b["qkv"].transpose(1, 0, 2, 3).reshape(C, 3 * d), torch.bfloat16)
+        mc, ml = int(np.diff(b["coff"]).max()), int(max(b["lens"]))
+        ws = torch.empty(max(16, G.attn_qcached_workspace_size(len(b["rows"]), C, H, 64, mc, ml)), dtype=torch.uint8, device="cuda")
+        o = torch.zeros(C, d, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(H, C, dtype=torch.float32, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        args = (_dev(b["coff"], torch.int32), mc, x, x[:, d:], x[:, 2 * d:], 3 * d, _dev(b["cache"]), _dev(b["rows"], torch.int64),
+                _dev(b["lens"], torch.int32), ml, _dev(b["tc"], torch.int64), H, 64, sp, st, 0.125, o, d, lse, ws, fmt, err)
+        calls.append((x, o, lse, err, args))
+    assert G.attn_qcached_workspace_size(1, 2, H, 64, 2, 700) > 0
+    graphs = []
+    side = torch.cuda.Stream()
+    for _, _, _, _, args in calls:
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            G.attn_fwd_qcached(*args)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            G.attn_fwd_qcached(*args)
+        graphs.append(g)
+    for rep in range(3):
+        for x, *_ in calls:
+            x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(rep)))
+        want = []
+        for _, o, lse, _, args in calls:
+            G.attn_fwd_qcached(*args)
+            want.append((o.clone(), lse.clone()))
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        for (_, o, lse, err, _), (wo, wl) in zip(calls, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+            assert G.check_error(err) == 0
+
+
+def test_python_refusals_on_the_gpu(G):
+    H, d = 2, 128
+    cache = torch.zeros(8, G.qcache_row_bytes(H, 64, G.QCACHE_INT8), dtype=torch.uint8, device="cuda")
+    k = torch.zeros(4, d, dtype=torch.bfloat16, device="cuda")
+    off, rows = _dev([0, 4], torch.int32), _dev([0], torch.int64)
+    pos, ts, err = _dev(range(4), torch.int32), _dev(range(4), torch.int64), _dev([0], torch.int32)
+
+    def append(**kw):
+        a = dict(off=off, k=k, v=k, stride=d, pos=pos, ts=ts, cache=cache, rows=rows, T=None)
+        a.update(kw)
+        G.qcache_append(a["off"], None, a["k"], a["v"], a["stride"], H, 64, a["pos"], a["ts"], a["cache"], a["rows"],
+                        G.QCACHE_INT8, err, T=a["T"])
+
+    append()
+    for kw in (dict(off=off.long()), dict(rows=rows.int()), dict(v=k.float()), dict(pos=pos.long()), dict(ts=ts.int()),
+               dict(cache=cache[:, :-16]), dict(pos=pos.cpu()), dict(off=off[:1]), dict(stride=2 * d), dict(T=5),
+               dict(k=k.half(), v=k.half()), dict(k=k[:, 4:])):
+        with pytest.raises(G.GenRankError):
+            append(**kw)
+    assert G.check_error(err) == 0
