@@ -23,70 +23,118 @@ namespace {
 constexpr int kWarps = 8;            // warps of a block
 constexpr int kMaxStageBytes = 64 << 10;  // staged rows of a block
 
-// The user that token row t belongs to, for ascending rows: a search for the first, then a walk.
-struct Cursor {
-  int u;
-  long long begin, end;  // rows [begin, end) of user u
-};
-
-GR_DEVICE void seek(Cursor& c, const int32_t* __restrict__ off, int B, long long t) {
-  c.u = warp_find_user(off, B, t);
-  c.begin = off[c.u];
-  c.end = off[c.u + 1];
-}
-
 // Whether user u's rows are usable, and where they start in the cache: offsets inside the
 // token array, no more rows than the user's segment, the cache range inside the cache and (for
 // a write) before the next user's, so that no two users write one row.
-GR_DEVICE bool user_rows(const QcacheArgs& a, int u, long long begin, long long end, bool write,
-                         int& n, long long& at) {
+template <bool kWrite>
+GR_DEVICE bool user_rows(const QcacheArgs& a, int u, int begin, int end, int& n, long long& at) {
   if (begin < 0 || end < begin || end > a.T) return false;
-  const long long seg = end - begin;
-  n = a.len ? a.len[u] : (int)seg;
+  n = a.len ? a.len[u] : end - begin;
   at = a.rows[u];
-  if (n < 0 || n > seg || at < 0 || at > a.R - n) return false;
-  return !write || u + 1 >= a.B || at + n <= a.rows[u + 1];
+  if (n < 0 || n > end - begin || at < 0 || at > a.R - n) return false;
+  return !kWrite || u + 1 >= a.B || at + n <= a.rows[u + 1];
 }
 
-// Codes of eight values as bytes 0..7 of two words: y = x inv + magic + bias lands the code,
-// rounded to nearest, in the low bits of y's pattern.  inv is 2^-14 (relative) above 1/s, so
-// that halves (|x| / s = k + 1/2, exact for these operands) round away from zero; every other
-// quotient is more than 1e-3 from a half (x has 8 significant bits, s at most 5), far beyond
-// that factor and the rounding of 1/s.
-GR_DEVICE uint2 code_bytes(const float* x, float inv, float magic) {
-  uint32_t z[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(fmaf(x[i], inv, magic));
-  const uint32_t a = __byte_perm(z[0], z[1], 0x0040), b = __byte_perm(z[2], z[3], 0x0040);
-  const uint32_t c = __byte_perm(z[4], z[5], 0x0040), d = __byte_perm(z[6], z[7], 0x0040);
-  return make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410));
+// A warp's walk over the token rows [t, t1) that have a cache row: a search for the first row's
+// user, then user by user.
+template <bool kWrite>
+struct Walk {
+  int u = -1;
+  int first = 0, last = 0, end = 0;  // the user's rows [first, last) are copied, [first, end) are its
+  long long at = 0;                  // cache row of token row 0 (first's less first)
+
+  // The first such row at or after t, or t1.
+  GR_DEVICE int next(const QcacheArgs& a, int t, int t1) {
+    while (t < t1) {
+      if (u < 0 || t >= end) {
+        u = u < 0 || t > end ? warp_find_user(a.off, a.B, t) : u + 1;
+        if (u >= a.B) return t1;  // rows behind the last user
+        first = a.off[u];
+        end = a.off[u + 1];
+        int n = 0;
+        last = user_rows<kWrite>(a, u, first, end, n, at) ? first + n : first;
+        at -= first;
+      }
+      if (t < first || t > end) return t1;  // offsets that do not ascend: flagged
+      if (t < last) return t;
+      t = end;
+    }
+    return t1;
+  }
+  GR_DEVICE long long row(int t) const { return at + t; }
+};
+
+// Every user's layout is checked by one lane of the grid.
+template <bool kWrite>
+GR_DEVICE void check_users(const QcacheArgs& a, int warps) {
+  const int stride = gridDim.x * warps * 32;
+  for (int u = blockIdx.x * warps * 32 + threadIdx.x; u < a.B; u += stride) {
+    int n;
+    long long at;
+    if (!user_rows<kWrite>(a, u, a.off[u], a.off[u + 1], n, at)) flag(a.err, GENRANK_DERR_LAYOUT);
+  }
 }
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
 constexpr float kHalfUp = 1.f + 1.f / 16384.f;
 
-// Scale s (its bf16 bits) and the factor inv of one head from its largest magnitude (bf16
-// bits; 0x7F80 and above: an infinity or a NaN among the values, whose head reads back as NaN).
-template <int FMT>
-GR_DEVICE uint32_t head_scale(uint32_t amax, float& inv) {
-  if (amax >= 0x7F80u) {
-    inv = 0.f;
-    return 0x7FC0u;
+// Codes of eight values (a vector of bf16) as bytes: x inv + magic + bias lands the code, rounded
+// to nearest, in the low bits of the sum's pattern.  inv is 2^-14 (relative) above 1/s, so that
+// halves (|x| / s = k + 1/2, exact for these operands) round away from zero; every other quotient
+// is more than 1e-3 from a half (x has 8 significant bits, s at most 5), far beyond that factor
+// and the rounding of 1/s.
+GR_DEVICE uint2 code_bytes(const uint4& w, float inv, float magic) {
+  const uint64_t i2 = f2_pack(inv, inv), m2 = f2_pack(magic, magic);
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f2_fma(f2_pack(bf16_lo(v[i]), bf16_hi(v[i])), i2, m2), lo, hi);
+    b[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
   }
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
+}
+
+// Scale s and the factor inv of one head from its largest magnitude (bf16 bits, finite).
+template <int FMT>
+GR_DEVICE float head_scale(uint32_t amax, float& inv) {
   const uint32_t bits = amax << 16;
   if constexpr (FMT == GENRANK_QCACHE_INT8) {
     // a = m 2^E, m in [1/2, 1): s = 2^(E-7), one more when m > 127/128 (the added bits carry)
-    int e = (int)((bits + 0x1FFFFu) >> 23) - 133;
-    e = min(max(e, -126), 121);
+    const int e = min(max((int)((bits + 0x1FFFFu) >> 23) - 133, -126), 121);
     inv = __uint_as_float((uint32_t)(127 - e) << 23) * kHalfUp;
-    return (uint32_t)(e + 127) << 7;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
   } else {
-    const float t = __fdiv_rn(__uint_as_float(bits), 7.f);
-    const uint32_t r = (__float_as_uint(t) + 0x40000u) & ~0x7FFFFu;
-    const float s = fminf(fmaxf(__uint_as_float(r), 0x1p-126f), 0x1.2p125f);
-    inv = __fdiv_rn(1.f, s) * kHalfUp;
-    return __float_as_uint(s) >> 16;
+    // a product in place of the division: a / 7 is halfway between two scales only where it is a
+    // whole number, which the product reaches (1/7 rounds up), and nowhere near otherwise
+    const float t = __uint_as_float(bits) * (1.f / 7.f);
+    const float s = fminf(fmaxf(__uint_as_float((__float_as_uint(t) + 0x40000u) & ~0x7FFFFu), 0x1p-126f), 0x1.2p125f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv *= kHalfUp;
+    return s;
   }
+}
+
+GR_DEVICE uint32_t max_magnitude(const uint4& w) {  // of 8 bf16, as bits; beyond 0x7F80 for a NaN
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t x = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+  return max(x & 0xFFFFu, x >> 16);
+}
+
+constexpr uint32_t kTop = 0x7F7Fu;  // the largest finite bf16
+
+// A vector whose head holds the largest magnitude (|c| <= 127 against the largest int8 scale) or
+// is not finite (codes 0).
+GR_DEVICE uint4 tame(const uint4& w, uint32_t amax) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if (amax > kTop) return r;
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // 254 * 2^120 in place of 255 * 2^120
+    o[i] = (v[i] & 0x80008000u) | __vminu2(v[i] & 0x7FFF7FFFu, 0x7F7E7F7Eu);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename Tin>
@@ -101,173 +149,202 @@ GR_DEVICE uint4 load_bf16x8(const Tin* p) {
   }
 }
 
-// Quantises eight values a lane (one head: 8 consecutive lanes) into the staged row.
+// Quantises vector i of the keys and of the values of a row (one head: 8 consecutive lanes, of
+// which lanes past the row's vectors hold zeros) into the staged row.
 template <int FMT>
-GR_DEVICE void put_head(uint8_t* row, const QRow& L, int H, int vec, const uint4& w, bool on) {
-  const uint32_t m = 0x7FFF7FFFu;
-  uint32_t mx = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+GR_DEVICE void put_vectors(uint8_t* row, const QRow& L, int i, uint4 k, uint4 v, bool on) {
+  uint32_t mx = max_magnitude(k) | (max_magnitude(v) << 16);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const uint32_t amax = max(mx & 0xffffu, mx >> 16);
-  float inv;
-  const uint32_t s = head_scale<FMT>(amax, inv);
-  if (!on) return;
-  float x[8];
-  Elem<__nv_bfloat16>::unpack(w, x);
-  constexpr float kBias = FMT == GENRANK_QCACHE_INT8 ? 128.f : 8.f;
-  if (s == 0x7FC0u || s == 0x7C00u) {  // not finite: codes 0; the largest int8 scale: |c| <= 127
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = s == 0x7FC0u ? 0.f : fminf(fmaxf(x[i], -3.3762e38f), 3.3762e38f);  // 127 * 2^121
-  }
-  const uint2 c = code_bytes(x, inv, kMagic + kBias);
-  const int head2 = vec >> 3;  // heads of K, then of V
-  if constexpr (FMT == GENRANK_QCACHE_INT8) {
-    *reinterpret_cast<uint2*>(row + vec * 8) = c;
+  uint32_t ak = mx & 0xFFFFu, av = mx >> 16;
+  float ki, vi, ks, vs;
+  if (max(ak, av) >= kTop) {
+    k = tame(k, ak);
+    v = tame(v, av);
+    ks = ak > kTop ? __uint_as_float(0x7FC00000u) : head_scale<FMT>(ak, ki);
+    vs = av > kTop ? __uint_as_float(0x7FC00000u) : head_scale<FMT>(av, vi);
+    if (ak > kTop) ki = 0.f;
+    if (av > kTop) vi = 0.f;
   } else {
-    const uint32_t a = c.x | (c.x >> 4), b = c.y | (c.y >> 4);
-    *reinterpret_cast<uint32_t*>(row + vec * 4) = __byte_perm(a, b, 0x6420);
+    ks = head_scale<FMT>(ak, ki);
+    vs = head_scale<FMT>(av, vi);
   }
-  if ((vec & 7) == 0) {
-    const int side = head2 >= H;
-    *reinterpret_cast<uint16_t*>(row + L.scales + (head2 - side * H) * 4 + side * 2) = (uint16_t)s;
+  constexpr float kBias = FMT == GENRANK_QCACHE_INT8 ? 128.f : 8.f;
+  const uint2 ck = code_bytes(k, ki, kMagic + kBias), cv = code_bytes(v, vi, kMagic + kBias);
+  if (!on) return;
+  if constexpr (FMT == GENRANK_QCACHE_INT8) {
+    *reinterpret_cast<uint2*>(row + i * 8) = ck;
+    *reinterpret_cast<uint2*>(row + L.scales / 2 + i * 8) = cv;
+  } else {
+    *reinterpret_cast<uint32_t*>(row + i * 4) = __byte_perm(ck.x | (ck.x >> 4), ck.y | (ck.y >> 4), 0x6420);
+    *reinterpret_cast<uint32_t*>(row + L.scales / 2 + i * 4) =
+        __byte_perm(cv.x | (cv.x >> 4), cv.y | (cv.y >> 4), 0x6420);
   }
+  if ((i & 7) == 0)
+    *reinterpret_cast<uint32_t*>(row + L.scales + i / 2) =
+        __byte_perm(__float_as_uint(ks), __float_as_uint(vs), 0x7632);
 }
 
-// k, v rows -> cache rows.  Each row is built in shared memory and leaves as whole 16-byte
-// vectors (pads included, so that a row's bytes are defined).
-template <typename Tin, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) k_qcache_append(const __grid_constant__ QcacheArgs a,
-                                                               int warps, long long run) {
+// k, v rows -> cache rows.  A piece is 64 of the 8H eight-value vectors of a row's keys and of its
+// values, two of each a lane (8 heads: the row); the next piece's loads are in flight while one
+// is worked on.  Each row is built in shared memory and leaves as whole 16-byte vectors (pads
+// included, so that a row's bytes are defined).  kOne: up to 8 heads, one piece a row.
+template <typename Tin, int FMT, bool kOne>
+__global__ void __launch_bounds__(kWarps * 32, kOne ? 4 : 1)
+    k_qcache_append(const __grid_constant__ QcacheArgs a, int warps, int run) {
   extern __shared__ __align__(16) uint8_t stage_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp >= warps) return;
   const QRow L = qrow(a.H, FMT);
   uint8_t* row = stage_all + (size_t)warp * L.bytes;
-  const int nv = 8 * a.H;  // 16-byte (bf16) vectors of one side
-  const long long t0 = ((long long)blockIdx.x * warps + warp) * run;
-  const long long t1 = min(t0 + run, a.T);
-  if (blockIdx.x == 0 && warp == 0) {  // every user's layout is checked once
-    for (int u = lane; u < a.B; u += 32) {
-      int n;
-      long long at;
-      if (!user_rows(a, u, a.off[u], a.off[u + 1], true, n, at)) flag(a.err, GENRANK_DERR_LAYOUT);
-    }
-    __syncwarp();
-  }
-  if (t0 >= t1) return;
+  const int nv = 8 * a.H;  // vectors of one side
+  const int pieces = kOne ? 1 : (nv + 63) / 64;
+  const long long from = ((long long)blockIdx.x * warps + warp) * run;
+  const int t0 = (int)min(from, a.T), t1 = (int)min(from + run, a.T);
   for (int i = lane; i < (L.bytes - L.scales) / 4; i += 32)
     *reinterpret_cast<uint32_t*>(row + L.scales + 4 * i) = 0u;
   __syncwarp();
-  Cursor c{0, 0, 0};
-  bool ok = false;
-  int n = 0;
-  long long at = 0;
-  for (long long t = t0; t < t1; ++t) {
-    if (t == t0 || t >= c.end) {
-      seek(c, a.off, a.B, t);
-      ok = t >= c.begin && t < c.end && user_rows(a, c.u, c.begin, c.end, true, n, at);
-      if (c.u == a.B - 1 && t >= c.end) break;  // rows behind the last user
-    }
-    if (!ok || t - c.begin >= n) continue;
+  Walk<true> walk;
+  uint4 k[2], v[2];
+  int64_t time = 0;
+  int32_t pos = 0;
+  auto load = [&](int t, int piece) {
     const Tin* kr = reinterpret_cast<const Tin*>(a.k) + t * a.tok_stride;
     const Tin* vr = reinterpret_cast<const Tin*>(a.v) + t * a.tok_stride;
-    for (int i0 = 0; i0 < 2 * nv; i0 += 128) {
-      uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j + lane;
-        w[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < 2 * nv) w[j] = load_bf16x8<Tin>((i < nv ? kr + 8 * i : vr + 8 * (i - nv)));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j + lane;
-        if (i0 + 32 * j < 2 * nv) put_head<FMT>(row, L, a.H, i, w[j], i < 2 * nv);
+    for (int j = 0; j < 2; ++j) {
+      const int i = 64 * piece + 32 * j + lane;
+      k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < nv) {
+        k[j] = load_bf16x8<Tin>(kr + 8 * i);
+        v[j] = load_bf16x8<Tin>(vr + 8 * i);
       }
     }
     if (lane == 0) {
-      *reinterpret_cast<int64_t*>(row + L.tail) = a.ts[t];
-      *reinterpret_cast<int32_t*>(row + L.tail + 8) = a.pos[t];
+      time = a.ts[t];
+      pos = a.pos[t];
     }
-    __syncwarp();
-    uint4* dst = reinterpret_cast<uint4*>(a.cache + (at + (t - c.begin)) * L.bytes);
-    for (int i = lane; i < L.bytes / 16; i += 32) dst[i] = reinterpret_cast<const uint4*>(row)[i];
-    __syncwarp();
+  };
+  int t = walk.next(a, t0, t1);
+  int piece = 0;  // stays 0 in the one-piece form
+  if (t < t1) load(t, 0);
+  while (t < t1) {
+    uint4 k_now[2] = {k[0], k[1]}, v_now[2] = {v[0], v[1]};
+    const int64_t time_now = time;
+    const int32_t pos_now = pos;
+    const int piece_now = piece;
+    uint4* dst = reinterpret_cast<uint4*>(a.cache + walk.row(t) * L.bytes);
+    if (kOne || ++piece == pieces) {
+      piece = 0;
+      t = walk.next(a, t + 1, t1);
+    }
+    if (t < t1) load(t, piece);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = 64 * piece_now + 32 * j + lane;
+      if (i - lane < nv) put_vectors<FMT>(row, L, i, k_now[j], v_now[j], i < nv);
+    }
+    if (piece_now == pieces - 1) {
+      if (lane == 0) {
+        *reinterpret_cast<int64_t*>(row + L.tail) = time_now;
+        *reinterpret_cast<int32_t*>(row + L.tail + 8) = pos_now;
+      }
+      __syncwarp();
+      for (int i = lane; i < L.bytes / 16; i += 32) dst[i] = reinterpret_cast<const uint4*>(row)[i];
+      __syncwarp();
+    }
   }
+  check_users<true>(a, warps);
 }
 
-// cache rows -> k, v rows (every value exact in bf16 and fp32)
-template <typename Tout, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) k_qcache_read(const __grid_constant__ QcacheArgs a,
-                                                             int warps, long long run) {
+// cache rows -> k, v rows (every value exact in bf16 and fp32); a lane writes 16 bytes at a time,
+// so that a warp's stores are whole lines in either type.
+template <typename Tout, int FMT, bool kOne>
+__global__ void __launch_bounds__(kWarps * 32, kOne ? 4 : 1)
+    k_qcache_read(const __grid_constant__ QcacheArgs a, int warps, int run) {
+  constexpr int kVals = 16 / sizeof(Tout);  // values of a vector
+  constexpr int kVecs = 32 / kVals;         // vectors of a lane in a piece (8 heads: the row)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const QRow L = qrow(a.H, FMT);
-  const int nv = 8 * a.H;
-  const long long t0 = ((long long)blockIdx.x * warps + warp) * run;
-  const long long t1 = min(t0 + run, a.T);
-  if (blockIdx.x == 0 && warp == 0) {
-    for (int u = lane; u < a.B; u += 32) {
-      int n;
-      long long at;
-      if (!user_rows(a, u, a.off[u], a.off[u + 1], false, n, at)) flag(a.err, GENRANK_DERR_LAYOUT);
+  const int nv = kQDh / kVals * a.H;
+  const int pieces = kOne ? 1 : (2 * nv + 32 * kVecs - 1) / (32 * kVecs);
+  const long long from = ((long long)blockIdx.x * warps + warp) * run;
+  const int t0 = (int)min(from, a.T), t1 = (int)min(from + run, a.T);
+  Walk<false> walk;
+  uint2 w[kVecs];      // codes
+  uint16_t sc[kVecs];  // scales
+  int4 tail = make_int4(0, 0, 0, 0);
+  auto load = [&](int t, int piece) {
+    const uint8_t* row = a.cache + walk.row(t) * L.bytes;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = 32 * (kVecs * piece + j) + lane;
+      w[j] = make_uint2(0u, 0u);
+      sc[j] = 0;
+      if (i < 2 * nv) {
+        const int side = i >= nv, head = (i - side * nv) / (kQDh / kVals);
+        sc[j] = __ldg(reinterpret_cast<const uint16_t*>(row + L.scales + head * 4 + side * 2));
+        constexpr int bytes = FMT == GENRANK_QCACHE_INT8 ? kVals : kVals / 2;
+        if constexpr (bytes == 8)
+          w[j] = __ldg(reinterpret_cast<const uint2*>(row + i * 8));
+        else if constexpr (bytes == 4)
+          w[j].x = __ldg(reinterpret_cast<const uint32_t*>(row + i * 4));
+        else
+          w[j].x = __ldg(reinterpret_cast<const uint16_t*>(row + i * 2));
+      }
     }
-    __syncwarp();
-  }
-  Cursor c{0, 0, 0};
-  bool ok = false;
-  int n = 0;
-  long long at = 0;
-  for (long long t = t0; t < t1; ++t) {
-    if (t == t0 || t >= c.end) {
-      seek(c, a.off, a.B, t);
-      ok = t >= c.begin && t < c.end && user_rows(a, c.u, c.begin, c.end, false, n, at);
-      if (c.u == a.B - 1 && t >= c.end) break;  // rows behind the last user
+    if (lane == 0) tail = __ldg(reinterpret_cast<const int4*>(row + L.tail));
+  };
+  int t = walk.next(a, t0, t1);
+  int piece = 0;  // stays 0 in the one-piece form
+  if (t < t1) load(t, 0);
+  while (t < t1) {
+    uint2 x[kVecs];
+    uint16_t s16[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      x[j] = w[j];
+      s16[j] = sc[j];
     }
-    if (!ok || t - c.begin >= n) continue;
-    const uint8_t* row = a.cache + (at + (t - c.begin)) * L.bytes;
-    Tout* kr = reinterpret_cast<Tout*>(a.k_out) + t * a.tok_stride;
-    Tout* vr = reinterpret_cast<Tout*>(a.v_out) + t * a.tok_stride;
-#pragma unroll 4
-    for (int i = lane; i < 2 * nv; i += 32) {
-      const int side = i >= nv, head = (i - side * nv) >> 3;
-      const float s = __uint_as_float(
-          (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row + L.scales + head * 4 + side * 2)) << 16);
-      uint2 w;
-      if constexpr (FMT == GENRANK_QCACHE_INT8) {
-        w = __ldg(reinterpret_cast<const uint2*>(row + i * 8));
-      } else {
-        const uint32_t p = __ldg(reinterpret_cast<const uint32_t*>(row + i * 4));
-        const uint32_t lo = p & 0x0F0F0F0Fu, hi = (p >> 4) & 0x0F0F0F0Fu;  // even, odd values
-        w = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+    const int4 tail_now = tail;
+    const int tok = t;
+    const int piece_now = piece;
+    if (kOne || ++piece == pieces) {
+      piece = 0;
+      t = walk.next(a, t + 1, t1);
+    }
+    if (t < t1) load(t, piece);
+    Tout* kr = reinterpret_cast<Tout*>(a.k_out) + tok * a.tok_stride;
+    Tout* vr = reinterpret_cast<Tout*>(a.v_out) + tok * a.tok_stride;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = 32 * (kVecs * piece_now + j) + lane;
+      if (i >= 2 * nv) break;
+      uint2 b = x[j];  // a byte per value
+      if constexpr (FMT == GENRANK_QCACHE_INT4) {
+        const uint32_t lo = b.x & 0x0F0F0F0Fu, hi = (b.x >> 4) & 0x0F0F0F0Fu;  // even, odd values
+        b = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
       }
       constexpr float kBias = FMT == GENRANK_QCACHE_INT8 ? 128.f : 8.f;
-      float f[8];
+      const float s = __uint_as_float((uint32_t)s16[j] << 16);
+      float f[kVals];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t word = e < 4 ? w.x : w.y;
+      for (int e = 0; e < kVals; ++e) {
         // a byte under the exponent of 2^23 reads as 2^23 + byte
-        const float y = __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u | (e & 3)));
+        const float y = __uint_as_float(__byte_perm(e < 4 ? b.x : b.y, 0x4B000000u, 0x7440u | (e & 3)));
         f[e] = (y - (8388608.f + kBias)) * s;
       }
-      Tout* dst = side ? vr + 8 * (i - nv) : kr + 8 * i;
-      if constexpr (sizeof(Tout) == 2) {
-        *reinterpret_cast<uint4*>(dst) = Elem<__nv_bfloat16>::pack(f);
-      } else {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
-      }
+      *reinterpret_cast<uint4*>(i < nv ? kr + kVals * i : vr + kVals * (i - nv)) = Elem<Tout>::pack(f);
     }
-    if (lane == 0) {
-      const int4 tail = __ldg(reinterpret_cast<const int4*>(row + L.tail));
-      if (a.ts_out) a.ts_out[t] = (int64_t)(((uint64_t)(uint32_t)tail.y << 32) | (uint32_t)tail.x);
-      if (a.pos_out) a.pos_out[t] = tail.z;
+    if (lane == 0 && piece_now == 0) {
+      if (a.ts_out) a.ts_out[tok] = (int64_t)(((uint64_t)(uint32_t)tail_now.y << 32) | (uint32_t)tail_now.x);
+      if (a.pos_out) a.pos_out[tok] = tail_now.z;
     }
   }
+  check_users<false>(a, warps);
 }
 
-template <typename T, int FMT>
-int launch(const QcacheArgs& a, bool write, cudaStream_t st) {
+template <typename T, int FMT, bool kOne>
+int launch_one(const QcacheArgs& a, bool write, cudaStream_t st) {
   static DeviceOnce smem_attr;
   const int sms = sm_count_current();
   if (sms <= 0) return GENRANK_ERR_CUDA;
@@ -275,18 +352,23 @@ int launch(const QcacheArgs& a, bool write, cudaStream_t st) {
   int warps = kWarps;
   if (write) {
     while (warps > 1 && warps * L.bytes > kMaxStageBytes) warps /= 2;
-    if (!set_smem_limit_once(smem_attr, (const void*)k_qcache_append<T, FMT>, kMaxStageBytes))
+    if (!set_smem_limit_once(smem_attr, (const void*)k_qcache_append<T, FMT, kOne>, kMaxStageBytes))
       return GENRANK_ERR_CUDA;
   }
-  // a run of consecutive rows per warp once every SM has its 64 warps
-  const long long most = (long long)sms * 64;
+  // a run of consecutive rows per warp once every SM has its 32 warps four times over
+  const long long most = (long long)sms * 128;
   const long long run = (a.T + most - 1) / most;
   const long long blocks = (a.T + run * warps - 1) / (run * warps);
   if (write)
-    k_qcache_append<T, FMT><<<(unsigned)blocks, warps * 32, warps * L.bytes, st>>>(a, warps, run);
+    k_qcache_append<T, FMT, kOne><<<(unsigned)blocks, warps * 32, warps * L.bytes, st>>>(a, warps, (int)run);
   else
-    k_qcache_read<T, FMT><<<(unsigned)blocks, warps * 32, 0, st>>>(a, warps, run);
+    k_qcache_read<T, FMT, kOne><<<(unsigned)blocks, warps * 32, 0, st>>>(a, warps, (int)run);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
+}
+
+template <typename T, int FMT>
+int launch(const QcacheArgs& a, bool write, cudaStream_t st) {
+  return a.H <= 8 ? launch_one<T, FMT, true>(a, write, st) : launch_one<T, FMT, false>(a, write, st);
 }
 
 int dispatch(const QcacheArgs& a, bool write, cudaStream_t st) {

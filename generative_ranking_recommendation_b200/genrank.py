@@ -9,6 +9,7 @@ fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -364,32 +365,45 @@ def attn_fwd_cached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, hist_off
     _check(rc, "genrank_attn_fwd_cached")
 
 
-def _need(what, dev, **tensors):
-    """The quantised cache's tensors: (tensor, dtype, least number of elements, contiguous) by
-    name, all on the CUDA device that the call is made on."""
-    if dev.type != "cuda":
-        raise GenRankError(f"{what}: tensors on {dev}: the library runs on a CUDA device")
-    if dev.index != torch.cuda.current_device():
-        raise GenRankError(f"{what}: tensors on {dev}, but the current device is "
+def _device_of(what, t):
+    """The CUDA device index of the call's tensors, which is the current device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise GenRankError(f"{what}: tensors on {t.device}: the library runs on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise GenRankError(f"{what}: tensors on cuda:{dev}, but the current device is "
                            f"cuda:{torch.cuda.current_device()}")
-    for name, (t, dtype, least, contiguous) in tensors.items():
-        if t is None:
-            continue
-        if t.device != dev:
-            raise GenRankError(f"{what}: {name} is on {t.device}, not on {dev}")
-        if t.dtype != dtype:
-            raise GenRankError(f"{what}: {name} must be {dtype}, not {t.dtype}")
-        if t.numel() < least or (contiguous and not t.is_contiguous()):
-            raise GenRankError(f"{what}: {name} must be contiguous with at least {least} elements")
+    return dev
 
 
-def _need_rows(what, name, t, rows, stride, width):
-    """A matrix given by its first element and a row stride stays inside its storage."""
-    if rows > 0 and (t.storage_offset() + (rows - 1) * stride + width) * t.element_size() > \
-            t.untyped_storage().nbytes():
-        raise GenRankError(f"{what}: {name} has fewer than {rows} rows of stride {stride}")
+def _vec(what, name, t, dev, dtype, least):
+    """The address of a contiguous tensor of at least `least` elements on device dev."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < least or not t.is_contiguous():
+        raise GenRankError(f"{what}: {name} must be contiguous, {dtype}, on cuda:{dev}, with at "
+                           f"least {least} elements (got {t.dtype} {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
 
 
+def _mat(what, name, t, dev, dtype, rows, stride, width):
+    """The address of a matrix given by its first element and a row stride, `rows` of whose rows
+    lie inside its storage."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise GenRankError(f"{what}: {name} must be {dtype} on cuda:{dev} (got {t.dtype} on {t.device})")
+    if rows > 0 and not (t.dim() == 2 and t.shape[0] >= rows and t.stride(0) == stride
+                         and t.shape[1] >= width and t.stride(1) == 1):
+        end = (t.storage_offset() + (rows - 1) * stride + width) * t.element_size()
+        if end > t.untyped_storage().nbytes():
+            raise GenRankError(f"{what}: {name} has fewer than {rows} rows of {width} values, "
+                               f"{stride} apart")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _slopes(xs):
+    return (ctypes.c_float * len(xs))(*xs)
+
+
+@functools.lru_cache(maxsize=1024)
 def qcache_row_bytes(H, dh, fmt) -> int:
     """Bytes of one row (one token) of a quantised history cache: allocate it as a uint8 tensor
     [rows, qcache_row_bytes(H, dh, fmt)].  fmt: QCACHE_INT8 or QCACHE_INT4."""
@@ -399,21 +413,11 @@ def qcache_row_bytes(H, dh, fmt) -> int:
     return n
 
 
-def _qcache_checks(what, offsets, length, k, v, tok_stride, H, dh, pos, ts, cache, rows, fmt,
-                   dev_err, T):
-    B, dev, rb = rows.numel(), k.device, qcache_row_bytes(H, dh, fmt)
+def _cache(what, cache, dev, H, dh, fmt):
+    rb = qcache_row_bytes(H, dh, fmt)
     if cache.dim() != 2 or cache.shape[1] != rb:
         raise GenRankError(f"{what}: cache must be uint8 [rows, {rb}]")
-    if v.dtype != k.dtype:
-        raise GenRankError(f"{what}: k and v must share a dtype")
-    _need(what, dev, k=(k, k.dtype, 0, False), v=(v, k.dtype, 0, False),
-          offsets=(offsets, torch.int32, B + 1, True), length=(length, torch.int32, B, True),
-          pos=(pos, torch.int32, T, True), ts=(ts, torch.int64, T, True),
-          cache=(cache, torch.uint8, 0, True), rows=(rows, torch.int64, B, True),
-          dev_err=(dev_err, torch.int32, 1, True))
-    for name, t in (("k", k), ("v", v)):
-        _need_rows(what, name, t, T, tok_stride, H * dh)
-    return B
+    return _vec(what, "cache", cache, dev, torch.uint8, 0)
 
 
 def qcache_append(src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts, cache, rows, fmt,
@@ -422,13 +426,19 @@ def qcache_append(src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts, cache,
     src_len None) of k, v (bf16 or fp32 views, row stride tok_stride), pos and ts become cache
     rows rows[u] + i.  cache: uint8 [R, qcache_row_bytes(H, dh, fmt)]; rows: int64 [B],
     ascending; T (default: pos.numel()) rows of the token arrays."""
+    what = "qcache_append"
     T = pos.numel() if T is None else int(T)
-    B = _qcache_checks("qcache_append", src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts,
-                       cache, rows, fmt, dev_err, T)
+    B, dt, dev = rows.numel(), k.dtype, _device_of(what, k)
     rc = lib().genrank_qcache_append(
-        B, T, _ptr(src_offsets), _ptr(src_len), _ptr(k), _ptr(v), int(tok_stride), int(H),
-        int(dh), _dtype_code(k), _ptr(pos), _ptr(ts), int(fmt), _ptr(cache),
-        int(cache.shape[0]), _ptr(rows), _ptr(dev_err), _stream(stream))
+        B, T, _vec(what, "src_offsets", src_offsets, dev, torch.int32, B + 1),
+        None if src_len is None else _vec(what, "src_len", src_len, dev, torch.int32, B),
+        _mat(what, "k", k, dev, dt, T, tok_stride, H * dh),
+        _mat(what, "v", v, dev, dt, T, tok_stride, H * dh), int(tok_stride), int(H), int(dh),
+        _dtype_code(k),
+        _vec(what, "pos", pos, dev, torch.int32, T), _vec(what, "ts", ts, dev, torch.int64, T),
+        int(fmt), _cache(what, cache, dev, H, dh, fmt), cache.shape[0],
+        _vec(what, "rows", rows, dev, torch.int64, B),
+        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream(stream))
     _check(rc, "genrank_qcache_append")
 
 
@@ -437,13 +447,19 @@ def qcache_read(dst_offsets, dst_len, cache, rows, k, v, tok_stride, H, dh, pos,
     """genrank_qcache_read: cache rows rows[u] + i (i < dst_len[u], or the whole segment) become
     rows dst_offsets[u] + i of k and v (bf16 or fp32), pos and ts (either may be None).  T
     (default: k.shape[0]) rows of the outputs."""
+    what = "qcache_read"
     T = k.shape[0] if T is None else int(T)
-    B = _qcache_checks("qcache_read", dst_offsets, dst_len, k, v, tok_stride, H, dh, pos, ts,
-                       cache, rows, fmt, dev_err, T)
+    B, dt, dev = rows.numel(), k.dtype, _device_of(what, k)
     rc = lib().genrank_qcache_read(
-        B, T, _ptr(dst_offsets), _ptr(dst_len), _ptr(cache), int(cache.shape[0]), _ptr(rows),
-        int(H), int(dh), int(fmt), _ptr(k), _ptr(v), int(tok_stride), _dtype_code(k),
-        _ptr(pos), _ptr(ts), _ptr(dev_err), _stream(stream))
+        B, T, _vec(what, "dst_offsets", dst_offsets, dev, torch.int32, B + 1),
+        None if dst_len is None else _vec(what, "dst_len", dst_len, dev, torch.int32, B),
+        _cache(what, cache, dev, H, dh, fmt), cache.shape[0],
+        _vec(what, "rows", rows, dev, torch.int64, B), int(H), int(dh), int(fmt),
+        _mat(what, "k", k, dev, dt, T, tok_stride, H * dh),
+        _mat(what, "v", v, dev, dt, T, tok_stride, H * dh), int(tok_stride), _dtype_code(k),
+        None if pos is None else _vec(what, "pos", pos, dev, torch.int32, T),
+        None if ts is None else _vec(what, "ts", ts, dev, torch.int64, T),
+        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream(stream))
     _check(rc, "genrank_qcache_read")
 
 
@@ -461,29 +477,24 @@ def attn_fwd_qcached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, cache, 
     what = "attn_fwd_qcached"
     B = cand_offsets.numel() - 1
     C = o.shape[0] if C is None else int(C)
-    rb = qcache_row_bytes(H, dh, fmt)
-    if cache.dim() != 2 or cache.shape[1] != rb:
-        raise GenRankError(f"{what}: cache must be uint8 [rows, {rb}]")
-    if len(slope_pos) < H or len(slope_time) < H:
+    dt, dev, width = q_c.dtype, _device_of(what, q_c), H * dh
+    if len(slope_pos) != H or len(slope_time) != H:
         raise GenRankError(f"{what}: a slope for each of the {H} heads")
-    dt = q_c.dtype
-    _need(what, q_c.device, q_c=(q_c, dt, 0, False), k_c=(k_c, dt, 0, False),
-          v_c=(v_c, dt, 0, False), o=(o, dt, 0, False),
-          cand_offsets=(cand_offsets, torch.int32, 2, True),
-          cache=(cache, torch.uint8, 0, True), rows=(rows, torch.int64, B, True),
-          cache_len=(cache_len, torch.int32, B, True), ts_cand=(ts_cand, torch.int64, C, True),
-          lse=(lse, torch.float32, H * C, True), ws=(ws, torch.uint8, 0, True),
-          dev_err=(dev_err, torch.int32, 1, True))
-    for name, t in (("q_c", q_c), ("k_c", k_c), ("v_c", v_c)):
-        _need_rows(what, name, t, C, cand_stride, H * dh)
-    _need_rows(what, "o", o, C, o_stride, H * dh)
-    sp, st = _host_floats(slope_pos), _host_floats(slope_time)
     rc = lib().genrank_attn_fwd_qcached(
-        B, C, _ptr(cand_offsets), int(max_cand), _ptr(q_c), _ptr(k_c), _ptr(v_c),
-        int(cand_stride), _ptr(cache), int(cache.shape[0]), _ptr(rows), _ptr(cache_len),
-        int(max_len), _ptr(ts_cand), int(fmt), int(H), int(dh), ctypes.cast(sp, _P),
-        ctypes.cast(st, _P), float(scale), _dtype_code(q_c), _ptr(o), int(o_stride), _ptr(lse),
-        _ptr(ws), 0 if ws is None else ws.numel(), _ptr(dev_err), _stream(stream))
+        B, C, _vec(what, "cand_offsets", cand_offsets, dev, torch.int32, 2), int(max_cand),
+        _mat(what, "q_c", q_c, dev, dt, C, cand_stride, width),
+        _mat(what, "k_c", k_c, dev, dt, C, cand_stride, width),
+        _mat(what, "v_c", v_c, dev, dt, C, cand_stride, width), int(cand_stride),
+        _cache(what, cache, dev, H, dh, fmt), cache.shape[0],
+        _vec(what, "rows", rows, dev, torch.int64, B),
+        _vec(what, "cache_len", cache_len, dev, torch.int32, B), int(max_len),
+        _vec(what, "ts_cand", ts_cand, dev, torch.int64, C), int(fmt), int(H), int(dh),
+        _slopes(tuple(slope_pos)), _slopes(tuple(slope_time)), float(scale), _dtype_code(q_c),
+        _mat(what, "o", o, dev, dt, C, o_stride, width), int(o_stride),
+        None if lse is None else _vec(what, "lse", lse, dev, torch.float32, H * C),
+        None if ws is None else _vec(what, "ws", ws, dev, torch.uint8, 0),
+        0 if ws is None else ws.numel(), _vec(what, "dev_err", dev_err, dev, torch.int32, 1),
+        _stream(stream))
     _check(rc, "genrank_attn_fwd_qcached")
 
 
