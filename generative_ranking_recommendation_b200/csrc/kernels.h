@@ -223,6 +223,10 @@ struct QcachedAttnArgs {
   int max_len;
 };
 int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st);
+// its tensor-core form: items of a head, 128 candidates and one of `splits` ranges of `chunk` rows;
+// with part, the ranges' unjoined results
+int launch_qcached_tc(const QcachedAttnArgs& c, int ctiles, int splits, int chunk, float* part,
+                      cudaStream_t st);
 size_t attn_fwd_qcached_workspace(int B, long long C, int H, int max_cand, int max_len);
 
 int launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t st);

@@ -7,7 +7,8 @@
 
 namespace gr {
 
-constexpr int kQDh = 64;  // values per head
+constexpr int kQDh = 64;          // values per head
+constexpr int kQPart = kQDh + 2;  // floats of a joined range: O, then its maximum and sum
 
 // Byte offsets inside one row of H heads:
 //   [K codes H x cb][V codes H x cb][(K scale, V scale) bf16 x H][pad to 16]

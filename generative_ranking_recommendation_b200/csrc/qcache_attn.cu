@@ -42,7 +42,6 @@ constexpr int kThreads = (kHeads + 2) * 32;
 constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
 constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
 constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
-constexpr int kPart = kQDh + 2;  // floats of a range's result: O, max, sum
 
 struct Params {
   QcachedAttnArgs c;
@@ -50,7 +49,7 @@ struct Params {
   int ctiles;  // candidate tiles of a user
   int splits;  // ranges of the history
   int chunk;   // rows of a range, a multiple of 64
-  float* part;  // [splits][C][H][kPart], or null: one range, written in place
+  float* part;  // [splits][C][H][kQPart], or null: one range, written in place
 };
 
 struct Work {
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
         for (int d = 0; d < 8; ++d) x[d] = fmaf(ps, vf[d], x[d]);
       }
       if (P.part) {
-        float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kPart;
+        float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kQPart;
 #pragma unroll
         for (int d = 0; d < 4; ++d) *reinterpret_cast<float2*>(dst + 8 * g + 2 * d) = make_float2(x[2 * d], x[2 * d + 1]);
         if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(mx[nt][e], l);
@@ -576,8 +575,8 @@ __global__ void __launch_bounds__(kHeads * 32) k_qcached_join(const __grid_const
   if (h >= a.H || k >= m) return;
   const int splits = min(P.splits, max(1, (n + P.chunk - 1) / max(1, P.chunk)));
   const long long ci = c0 + k;
-  const float* src = P.part + (ci * a.H + h) * kPart;
-  const long long step = a.T * a.H * kPart;
+  const float* src = P.part + (ci * a.H + h) * kQPart;
+  const long long step = a.T * a.H * kQPart;
   const int half = lane >> 4, d = 4 * (lane & 15);
   float top = -INFINITY;
   for (int s = lane; s < splits; s += 32) top = fmaxf(top, src[s * step + kQDh]);
@@ -609,18 +608,25 @@ __global__ void __launch_bounds__(kHeads * 32) k_qcached_join(const __grid_const
 }
 
 struct Plan {
-  int nt, groups, ctiles, splits, chunk;
+  int nt;  // column tiles of 8 candidates, or 0: the tensor-core form with 128 candidates an item
+  int groups, ctiles, splits, chunk;
+  long long units;  // blocks, or items, of one range
 };
-// Blocks are one user's 8 heads and up to 32 candidates; while they do not fill the 148 SMs a few
-// times over, the history is cut into ranges of at least 64 rows.
+constexpr int kTcFrom = 33;  // bound of the candidates a user from which the tensor-core form runs
+
+// Blocks are one user's 8 heads and up to 32 candidates (tensor cores: items of a head and 128
+// candidates); while they do not fill the 148 SMs a few times over, the history is cut into ranges
+// of at least 64 (256) rows.
 Plan plan(int B, int H, int max_cand, int max_len) {
   Plan p;
-  p.nt = max_cand <= 8 ? 1 : max_cand <= 16 ? 2 : 4;
+  const bool tc = max_cand >= kTcFrom;
+  p.nt = tc ? 0 : max_cand <= 8 ? 1 : max_cand <= 16 ? 2 : 4;
   p.groups = (H + kHeads - 1) / kHeads;
-  p.ctiles = (max_cand + 8 * p.nt - 1) / (8 * p.nt);
-  const long long units = (long long)B * p.groups * (p.ctiles > 0 ? p.ctiles : 1);
-  const long long want = (148 * 4 + units - 1) / units;
-  const long long most = (max_len + 63) / 64;
+  const int tile = tc ? 128 : 8 * p.nt, least = tc ? 256 : 64;
+  p.ctiles = max_cand > tile ? (max_cand + tile - 1) / tile : 1;
+  p.units = (long long)B * (tc ? H : p.groups) * p.ctiles;
+  const long long want = (148 * 4 + p.units - 1) / p.units;
+  const long long most = (max_len + least - 1) / least;
   const long long s = want < most ? want : most;
   p.splits = s > 1 ? (int)s : 1;
   p.chunk = ((max_len + p.splits - 1) / p.splits + 63) / 64 * 64;
@@ -653,16 +659,14 @@ int launch_nt(const Params& P, int nt, unsigned blocks, cudaStream_t st) {
 
 size_t attn_fwd_qcached_workspace(int B, long long C, int H, int max_cand, int max_len) {
   const qca::Plan p = qca::plan(B, H, max_cand, max_len);
-  return p.splits > 1 ? (size_t)p.splits * C * H * qca::kPart * sizeof(float) : 0;
+  return p.splits > 1 ? (size_t)p.splits * C * H * kQPart * sizeof(float) : 0;
 }
 
 int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   using namespace qca;
   const Plan p = plan(c.a.B, c.a.H, c.max_cand, c.max_len);
-  if (p.ctiles == 0) return GENRANK_OK;
-  const long long units = (long long)c.a.B * p.groups * p.ctiles;
   const long long joins = (long long)c.a.B * p.groups * c.max_cand;
-  if (units * p.splits > INT32_MAX || joins > INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  if (p.units * p.splits > INT32_MAX || joins > INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
   Params P;
   P.c = c;
   P.groups = p.groups;
@@ -670,9 +674,10 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   P.splits = p.splits;
   P.chunk = p.chunk;
   P.part = p.splits > 1 ? (float*)c.a.ws : nullptr;
-  const unsigned blocks = (unsigned)(units * p.splits);
-  const int rc = c.format == GENRANK_QCACHE_INT8 ? launch_nt<GENRANK_QCACHE_INT8>(P, p.nt, blocks, st)
-                                                 : launch_nt<GENRANK_QCACHE_INT4>(P, p.nt, blocks, st);
+  const unsigned blocks = (unsigned)(p.units * p.splits);
+  const int rc = p.nt == 0 ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
+                 : c.format == GENRANK_QCACHE_INT8 ? launch_nt<GENRANK_QCACHE_INT8>(P, p.nt, blocks, st)
+                                                   : launch_nt<GENRANK_QCACHE_INT4>(P, p.nt, blocks, st);
   if (rc != GENRANK_OK || p.splits == 1) return rc;
   k_qcached_join<<<(unsigned)joins, kHeads * 32, 0, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
