@@ -612,7 +612,7 @@ struct Plan {
   int groups, ctiles, splits, chunk;
   long long units;  // blocks, or items, of one range
 };
-constexpr int kTcFrom = 33;  // bound of the candidates a user from which the tensor-core form runs
+constexpr int kTcFrom = 49;  // bound of the candidates a user from which the tensor-core form runs
 
 // Blocks are one user's 8 heads and up to 32 candidates (tensor cores: items of a head and 128
 // candidates); while they do not fill the 148 SMs a few times over, the history is cut into ranges

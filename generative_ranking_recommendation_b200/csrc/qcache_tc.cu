@@ -716,12 +716,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         const int at = 4 * i + sub, row = 32 * w4 + at;
         uint4* place = chunk_at(smem + kOffQ + qb * kQBytes, row, ch);
         const uint4 q4 = *place;
-        float f[8], kf[8];
-        Elem<__nv_bfloat16>::unpack(q4, f);
-        Elem<__nv_bfloat16>::unpack(k4, kf);
-        float dot = 0.f;
+        const uint32_t qw[4] = {q4.x, q4.y, q4.z, q4.w}, kw[4] = {k4.x, k4.y, k4.z, k4.w};
+        uint64_t f2[4], dot2 = 0ull;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(f[e], kf[e], dot);
+        for (int e = 0; e < 4; ++e) {
+          f2[e] = f2_pack(bf16_lo(qw[e]), bf16_hi(qw[e]));
+          dot2 = f2_fma(f2[e], f2_pack(bf16_lo(kw[e]), bf16_hi(kw[e])), dot2);
+        }
+        float dot, dot_hi;
+        f2_unpack(dot2, dot, dot_hi);
+        dot += dot_hi;
         // the row's largest magnitude, as bf16 bits (an infinity or a NaN makes the row NaN anyhow)
         const uint32_t mk = 0x7FFF7FFFu;
         uint32_t top = __vmaxu2(__vmaxu2(q4.x & mk, q4.y & mk), __vmaxu2(q4.z & mk, q4.w & mk));
@@ -735,9 +739,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         qe = max(qe, -100 - nx.ke);
         const int up = min(qe + nx.ke, 126);
         const float qd = pow2(-qe);
-        const bool on = row < nx.mt;
+        float f[8];  // (rows past the item's candidates are never written out)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = on ? f[e] * qd : 0.f;
+        for (int e = 0; e < 4; ++e) f2_unpack(f2_mul(f2[e], f2_pack(qd, qd)), f[2 * e], f[2 * e + 1]);
         *place = FMT == GENRANK_QCACHE_INT4
                      ? make_uint4(pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7]))
                      : make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
@@ -792,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       const float total = fmaf(l, wa, ws);
       const float inv = P.part ? 1.f : 1.f / total;
       const float wo = wa * pow2(it.ve) * inv, wb = ws * inv;
+      const uint64_t wo2 = f2_pack(wo, wo), wb2 = f2_pack(wb, wb);
       float* part = P.part ? P.part + (((long long)it.s * a.T + ci) * a.H + it.h) * kQPart : nullptr;
 #pragma unroll 1
       for (int c0 = 0; c0 < kQDh; c0 += 16) {
@@ -800,14 +805,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         tmem_ld_wait(o);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float v[8], x[8];
+          float x[8];
           uint4* place = chunk_at(stage, lane, c0 / 8 + z);
-          Elem<__nv_bfloat16>::unpack(*place, v);
+          const uint4 v4 = *place;
+          const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = FMT == GENRANK_QCACHE_INT4 ? (e & 3) * 2 + (e >> 2) : e;  // of dimension e
-            const float oe = it.tiles > 0 ? __uint_as_float(o[8 * z + col]) * wo : 0.f;
-            x[e] = it.s == 0 ? fmaf(wb, v[e], oe) : oe;
+          for (int e = 0; e < 8; e += 2) {
+            const int lo = FMT == GENRANK_QCACHE_INT4 ? (e & 3) * 2 + (e >> 2) : e;  // columns of dimensions
+            const int hi = FMT == GENRANK_QCACHE_INT4 ? lo + 2 : e + 1;              // e and e + 1
+            uint64_t y = 0ull;
+            if (it.tiles > 0) y = f2_mul(f2_pack(__uint_as_float(o[8 * z + lo]), __uint_as_float(o[8 * z + hi])), wo2);
+            if (it.s == 0) y = f2_fma(f2_pack(bf16_lo(v[e / 2]), bf16_hi(v[e / 2])), wb2, y);
+            f2_unpack(y, x[e], x[e + 1]);
           }
           if (part) {
             if (row_ok)
