@@ -1,4 +1,5 @@
-// Candidate attention over the quantised history cache (sm_100a).
+// Candidate attention over the quantised history cache (sm_100a).  This is the form for few
+// candidates a user, and the choice between it and the one of qcache_tc.cu (plan, below).
 //
 // Candidate c of user u (position n + 1, time t_c) sees the user's n cached rows and itself:
 //   s_cj = scale q_c.k_j - m_h |n + 1 - p_j| - m_t,h |t_c - t_j|,   s_cc = scale q_c.k_c
@@ -9,15 +10,15 @@
 // are exact in fp16, so q.c has exact products and fp32 sums: no key is ever rounded.
 //
 // One pass over the rows with the running maximum and sum of an online softmax:
-//   * A block takes one user, up to 8 heads (a warp each), up to 32 candidates and a range of
-//     the history.  A row of the cache holds every head's keys and values next to one another,
+//   * A block takes one user, up to 8 heads (a warp each), up to 8 candidates and a range of the
+//     history.  A row of the cache holds every head's keys and values next to one another,
 //     so a tile of rows is one contiguous piece: one more warp copies tiles into a ring of
-//     shared-memory stages with bulk copies (wider models: a few per row), and another turns
-//     each row's time and position into two distances, once for all heads.
+//     shared-memory stages with bulk copies (wider models: a few per row), and turns each row's
+//     time and position into two distances, once for all heads.
 //   * A warp multiplies codes as the 16-row operand of m16n8k16 (keys for S^T = K q^T, head
 //     dimensions for O^T = V^T P^T), candidates in the 8 columns, so that one candidate wastes
-//     7/8 of a column tile and not 15/16 of a row tile; the work per row is the unpacking: three
-//     instructions per code pair, no conversions.  The candidate's P^T operand is S^T's
+//     7/8 of a column tile and not 15/16 of a row tile; the work per row is the unpacking: two or
+//     three instructions per code pair, no conversions.  The candidate's P^T operand is S^T's
 //     accumulator transposed 8 x 8 (movmatrix); the key order inside a tile is permuted so that
 //     the shared-memory reads of eight lanes fall into different banks for every row length.
 //   * V's scale is folded into P (p_j s_j, fp16 with a power-of-two range shift): 11 bits where
@@ -26,6 +27,9 @@
 //     candidate's own score: most tiles take one vote and no shuffles.
 //   * Short of blocks, the history is cut into ranges; the ranges' (max, sum, O) in fp32 are
 //     joined by a second kernel, always in the same order.
+// Bound: with one candidate the copies, at 256 users x 4096 rows of 8 heads 156 us for int4 rows
+// (587 MB, 3.8 TB/s; the copies alone take 117) and 211 us for int8 (1124 MB, 5.3 TB/s); with more
+// the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 88 us).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -37,8 +41,9 @@ namespace gr {
 namespace qca {
 
 constexpr int kHeads = 8;    // heads of a block, one warp each
+constexpr int kCands = 8;    // candidates of a block
 constexpr int kStages = 3;   // tiles in flight
-constexpr int kThreads = (kHeads + 2) * 32;
+constexpr int kThreads = (kHeads + 1) * 32;
 constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
 constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
 constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
@@ -114,6 +119,15 @@ GR_DEVICE uint32_t low_nibbles(uint32_t w) {  // nibbles 0 and 4
 GR_DEVICE uint32_t high_nibbles(uint32_t w) {  // nibbles 1 and 5: (1024 + 16 u) / 16 - 72
   return fma_f16((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
 }
+// The same of byte pairs 1024 + 16 u1 + u0, mostly on the FMA pipe: with 1 <= u0 <= 15 (a code is
+// never -8) the first rounding, to whole numbers, takes u0 off.  For keys, where the bytes come out
+// with one instruction each, it relieves the integer pipe (159.7 -> 155.6 us at 256 users x 4096
+// rows, one candidate); for values it does not pay.
+GR_DEVICE void byte_nibbles(uint32_t b, uint32_t& lo, uint32_t& hi) {
+  const uint32_t t = fma_f16(b, 0x2C002C00u, 0x63FF63FFu);  // b / 16 + 1023.5 = 1088 + u1
+  hi = sub_f16(t, 0x64486448u);                             // - 1096
+  lo = sub_f16(fma_f16(hi, 0xCC00CC00u, b), 0x64886488u);   // b - 16 hi = 1152 + u0, - 1160
+}
 GR_DEVICE uint32_t byte_pair(uint32_t w, uint32_t sel) {  // two bytes chosen by sel, - 1152
   return sub_f16(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
 }
@@ -139,10 +153,8 @@ GR_DEVICE void key_codes(const uint8_t* p, int t, uint32_t (&r)[4][2]) {
     const uint32_t ww[2] = {w.x, w.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r[2 * i][0] = low_nibbles(ww[i]);
-      r[2 * i][1] = high_nibbles(ww[i]);
-      r[2 * i + 1][0] = low_nibbles(ww[i] >> 8);
-      r[2 * i + 1][1] = high_nibbles(ww[i] >> 8);
+      byte_nibbles(__byte_perm(ww[i], 0x64646464u, 0x4240), r[2 * i][0], r[2 * i][1]);
+      byte_nibbles(__byte_perm(ww[i], 0x64646464u, 0x4341), r[2 * i + 1][0], r[2 * i + 1][1]);
     }
   } else {
     const uint2 a = *reinterpret_cast<const uint2*>(p + 8 * t);
@@ -197,9 +209,8 @@ GR_DEVICE float group_sum(float x) {
   return x;
 }
 
-// NT: column tiles of 8 candidates; SUB: a tile is 32 SUB rows, whose chains of loads, products
-// and exponentials overlap.
-template <int FMT, int NT, int SUB>
+// A tile is 32 SUB rows, whose chains of loads, products and exponentials overlap.
+template <int FMT, int SUB>
 __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Params P) {
   constexpr int kRows = 32 * SUB;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -219,8 +230,8 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   }
   if (threadIdx.x == 0 && (m > c.max_cand || n > c.max_len)) flag(a.err, GENRANK_DERR_LAYOUT);
   m = min(m, c.max_cand);
-  const int cb = c0 + w.ct * 8 * NT;               // the block's first candidate row
-  const int mt = min(c0 + m - cb, 8 * NT);         // and how many
+  const int cb = c0 + w.ct * kCands;               // the block's first candidate row
+  const int mt = min(c0 + m - cb, kCands);         // and how many
   const int lo = w.s * P.chunk, hi = min(min(n, c.max_len), lo + P.chunk);
   if (mt <= 0 || (w.s > 0 && lo >= hi)) return;
   const int tiles = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
@@ -240,15 +251,13 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   }
   __syncthreads();
 
+  const long long t_ref = a.ts[c0];
   if (warp == kHeads) {
-    // ------------------------------------------------------------------ copies
+    // ------------------------------------------------------------------ copies and distances
     const uint8_t* src = c.cache + (at + lo) * (long long)L.bytes;
     const int scale_bytes = (4 * heads + 15) / 16 * 16;
-    int i = 0;
-    for (; i < tiles; ++i) {
+    auto copy = [&](int i) {
       const int st = i % kStages;
-      const bool ok = i < kStages || mbar_wait(&empty[st], (i / kStages + 1) & 1, abort_flag, a.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
       const int rows = min(kRows, hi - lo - i * kRows);
       uint8_t* dst = smem + st * stage_bytes;
       const uint8_t* from = src + (long long)i * kRows * L.bytes;
@@ -269,22 +278,17 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
           bulk_load(to + S.tail, row + L.tail, 16, &full[st]);
         }
       }
-    }
-    // the copies issued last have landed before the block exits
-    if (lane == 0)
-      for (int x = max(0, i - kStages); x < i; ++x) mbar_drain(&full[x % kStages], (x / kStages) & 1);
-    return;
-  }
-  const long long t_ref = a.ts[c0];
-  if (warp == kHeads + 1) {
-    // ------------------------------------------------------------------ distances, a row a lane
+    };
+    int copied = 0;
+    for (; copied < min(tiles, kStages); ++copied) copy(copied);
     long long t_min = a.ts[cb + min(lane, mt - 1)];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, o));
     bool bad_time = false, bad_pos = false;
     for (int i = 0; i < tiles; ++i) {
+      // tile i's distances, a row a lane, then the copy that takes the place of tile i - 1
       const int st = i % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / kStages) & 1, abort_flag, a.err))) return;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / kStages) & 1, abort_flag, a.err))) break;
 #pragma unroll
       for (int z = 0; z < SUB; ++z) {
         const int r = 32 * z + lane;
@@ -303,9 +307,17 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[st]);
+      if (i > 0 && copied < tiles) {
+        const int pr = (i - 1) % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[pr], ((i - 1) / kStages) & 1, abort_flag, a.err))) break;
+        copy(copied++);
+      }
     }
     if (bad_time) flag(a.err, GENRANK_DERR_TS_ORDER);
     if (bad_pos) flag(a.err, GENRANK_DERR_POS_RANGE);
+    // the copies issued last have landed before the block exits
+    if (lane == 0)
+      for (int x = max(0, copied - kStages); x < copied; ++x) mbar_drain(&full[x % kStages], (x / kStages) & 1);
     return;
   }
   if (warp >= heads) return;
@@ -316,81 +328,66 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   const float sp2 = a.slope_pos[h] * kLog2e, st2 = a.slope_time[h] * kLog2e;
   const float sc2 = a.scale * kLog2e;
 
-  // q as the B operand (candidate 8 nt + g), scaled by a power of two into fp16's range, and
-  // each candidate's own score
-  uint32_t q[NT][4][2];
-  float self[NT][2];  // of candidates 8 nt + 2t, + 1: the lane's accumulator columns
+  // q as the B operand (candidate g), scaled by a power of two into fp16's range, and each
+  // candidate's own score
+  uint32_t q[4][2];
+  float self[2];  // of candidates 2t, 2t + 1: the lane's accumulator columns
   float qs;
   {
-    float qf[NT][16], own[NT];
-    float amax = 0.f;
+    const long long ci = cb + min(g, mt - 1);
+    const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + ci * a.tok_stride + h * kQDh;
+    const __nv_bfloat16* kr = (const __nv_bfloat16*)a.k + ci * a.tok_stride + h * kQDh;
+    const int d0 = dim_of<FMT>(t, 0, 0, 0), d1 = dim_of<FMT>(t, 2, 0, 0);
+    float qf[16], kf[16];
+    Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d0)), qf);
+    Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d1)), qf + 8);
+    Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d0)), kf);
+    Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d1)), kf + 8);
+    float dot = 0.f, amax = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int ci = cb + min(8 * nt + g, mt - 1);
-      const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + ci * a.tok_stride + h * kQDh;
-      const __nv_bfloat16* kr = (const __nv_bfloat16*)a.k + ci * a.tok_stride + h * kQDh;
-      const int d0 = dim_of<FMT>(t, 0, 0, 0), d1 = dim_of<FMT>(t, 2, 0, 0);
-      float kf[16];
-      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d0)), qf[nt]);
-      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + d1)), qf[nt] + 8);
-      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d0)), kf);
-      Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(kr + d1)), kf + 8);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        dot = fmaf(qf[nt][i], kf[i], dot);
-        const float x = fabsf(qf[nt][i]);
-        if (x < INFINITY) amax = fmaxf(amax, x);
-      }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      own[nt] = dot * sc2;
+    for (int i = 0; i < 16; ++i) {
+      dot = fmaf(qf[i], kf[i], dot);
+      const float x = fabsf(qf[i]);
+      if (x < INFINITY) amax = fmaxf(amax, x);
     }
+    dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+    dot += __shfl_xor_sync(0xffffffffu, dot, 2);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
     const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
     qs = __uint_as_float((uint32_t)(127 + ex) << 23) * sc2;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
+      for (int s = 0; s < 2; ++s) {
+        // elements of the 16 loaded (two runs of 8 dimensions)
+        const int i0 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 0);
+        const int i1 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 1);
+        q[ks][s] = pack_f16(qf[i0] * down, qf[i1] * down);
+      }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          // element of the 16 loaded (two runs of 8 dimensions)
-          const int i0 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 0);
-          const int i1 = 8 * (ks >> 1) + dim_of<FMT>(0, ks & 1, s, 1);
-          q[nt][ks][s] = pack_f16(qf[nt][i0] * down, qf[nt][i1] * down);
-        }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) self[nt][e] = __shfl_sync(0xffffffffu, own[nt], 4 * (2 * t + e));
-    }
+    for (int e = 0; e < 2; ++e) self[e] = __shfl_sync(0xffffffffu, dot * sc2, 4 * (2 * t + e));
   }
-  float row_term[NT][2], mx[NT][2];
-  uint64_t sum2[NT];  // pairs: the lane's two candidates
+  float row_term[2], mx[2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const long long tc = a.ts[cb + min(8 * nt + 2 * t + e, mt - 1)];
-      row_term[nt][e] = st2 * (float)(tc - t_ref);
-      self[nt][e] += row_term[nt][e];
-      mx[nt][e] = fmaxf(self[nt][e], kLowest);
-    }
-    sum2[nt] = 0ull;  // (+0, +0)
+  for (int e = 0; e < 2; ++e) {
+    const long long tc = a.ts[cb + min(2 * t + e, mt - 1)];
+    row_term[e] = st2 * (float)(tc - t_ref);
+    self[e] += row_term[e];
+    mx[e] = fmaxf(self[e], kLowest);
   }
+  uint64_t sum2 = 0ull;  // the lane's two candidates: (+0, +0)
 
-  float o[4][NT][4];  // dimension 8g + 2i (and + 1: elements 2, 3) of candidates 2t, 2t + 1
+  float o[4][4];  // dimension 8g + 2i (and + 1: elements 2, 3) of candidates 2t, 2t + 1
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   float v_top = 0.f, v_down = 0.f;  // power of two >= every V scale so far; 2^kVExp over it
   const int kr0 = key_row(g);                              // this lane's key row (scores)
   const int va = key_row(2 * t) * S.bytes, vb = key_row(2 * t + 1) * S.bytes;  // its pair of value rows
-  const int k_at = warp * S.cb + kr0 * S.bytes, sc_at = S.scales + 4 * warp + kr0 * S.bytes;
+  const int k_at = warp * S.cb + kr0 * S.bytes, sc_at = S.scales + 4 * warp;
   const int v_at = S.scales / 2 + warp * S.cb;
   int st = 0, ph = 0;
 
@@ -398,101 +395,98 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
     // the distances are there, and with them the rows that they were computed from
     if (!__all_sync(0xffffffffu, mbar_wait(&ready[st], ph, abort_flag, a.err))) return;
     const uint8_t* base = smem + st * stage_bytes;
-    const float4* gap = &gaps[st][kr0];
+
+    // each row's key scale, bias and value scale, a row a lane
+    float key_scale[SUB], key_bias[SUB], value_scale[SUB];
+    float v_max = 0.f;
+#pragma unroll
+    for (int z = 0; z < SUB; ++z) {
+      const int row = 32 * z + lane;
+      const uint32_t sc = *reinterpret_cast<const uint32_t*>(base + sc_at + row * S.bytes);
+      const float4 gp = gaps[st][row];
+      key_scale[z] = bf16_lo(sc) * qs;
+      key_bias[z] = fmaf(sp2, gp.x, fmaf(st2, gp.y, gp.z));
+      value_scale[z] = bf16_hi(sc);
+      v_max = fmaxf(v_max, value_scale[z]);
+    }
 
     // S^T = K q^T, its scale and bias
-    float s[2 * SUB][NT][4], vs[2 * SUB][2];
-    float v_max = 0.f;
+    float s[2 * SUB][4];
 #pragma unroll
     for (int kk = 0; kk < 2 * SUB; ++kk) {
       const uint8_t* ra = base + k_at + 16 * kk * S.bytes;
       uint32_t ka[4][2], kb[4][2];
       key_codes<FMT>(ra, t, ka);
       key_codes<FMT>(ra + S.bytes, t, kb);
-      float acc[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const uint32_t frag[4] = {ka[ks][0], kb[ks][0], ka[ks][1], kb[ks][1]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(acc[nt], frag, q[nt][ks][0], q[nt][ks][1]);
+        mma(acc, frag, q[ks][0], q[ks][1]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(base + sc_at + (16 * kk + e) * S.bytes);
-        const float4 gp = gap[16 * kk + e];
-        const float ksc = bf16_lo(sc) * qs;
-        const float col = fmaf(sp2, gp.x, fmaf(st2, gp.y, gp.z));
-        vs[kk][e] = bf16_hi(sc);
-        v_max = fmaxf(v_max, vs[kk][e]);
-        const uint64_t k2 = f2_pack(ksc, ksc), c2 = f2_pack(col, col);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          f2_unpack(f2_fma(f2_pack(acc[nt][2 * e], acc[nt][2 * e + 1]), k2, c2), s[kk][nt][2 * e],
-                    s[kk][nt][2 * e + 1]);
+        const int of = 16 * (kk & 1) + kr0 + e;
+        const float ksc = __shfl_sync(0xffffffffu, key_scale[kk / 2], of);
+        const float col = __shfl_sync(0xffffffffu, key_bias[kk / 2], of);
+        f2_unpack(f2_fma(f2_pack(acc[2 * e], acc[2 * e + 1]), f2_pack(ksc, ksc), f2_pack(col, col)), s[kk][2 * e],
+                  s[kk][2 * e + 1]);
       }
     }
 
     // the running maxima move (rarely: a score passed one by 2^kSlack, or a V scale is the
     // largest so far)
     bool move = v_max > v_top;
-    float best[NT][2];
+    float best[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      float x = fmaxf(s[0][e], s[0][e + 2]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
-#pragma unroll
-        for (int kk = 1; kk < 2 * SUB; ++kk) x = fmaxf(x, fmaxf(s[kk][nt][e], s[kk][nt][e + 2]));
-        best[nt][e] = x;
-        move |= x > mx[nt][e] + kSlack;
-      }
+      for (int kk = 1; kk < 2 * SUB; ++kk) x = fmaxf(x, fmaxf(s[kk][e], s[kk][e + 2]));
+      best[e] = x;
+      move |= x > mx[e] + kSlack;
+    }
     if (__any_sync(0xffffffffu, move)) {
       float vm = v_max < INFINITY ? v_max : 0.f;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
       const int ex = max((int)(__float_as_uint(vm) >> 23) - 126, -100);  // 2^ex > vm
       const float top = fmaxf(v_top, __uint_as_float((uint32_t)(ex + 127) << 23));
-      const float va_ = v_top > 0.f ? v_top / top : 1.f;
+      const float v_al = v_top > 0.f ? v_top / top : 1.f;
       v_top = top;
       v_down = (float)(1 << kVExp) / top;
+      float al[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float al[2];
+      for (int e = 0; e < 2; ++e) {
+        const float next = fmaxf(mx[e], group_max(best[e]));
+        al[e] = ex2(mx[e] - next);
+        mx[e] = next;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float next = fmaxf(mx[nt][e], group_max(best[nt][e]));
-          al[e] = ex2(mx[nt][e] - next);
-          mx[nt][e] = next;
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            o[d][nt][e] *= al[e] * va_;
-            o[d][nt][e + 2] *= al[e] * va_;
-          }
+        for (int d = 0; d < 4; ++d) {
+          o[d][e] *= al[e] * v_al;
+          o[d][e + 2] *= al[e] * v_al;
         }
-        sum2[nt] = f2_mul(sum2[nt], f2_pack(al[0], al[1]));
       }
+      sum2 = f2_mul(sum2, f2_pack(al[0], al[1]));
     }
 
     // P and O^T += V^T P^T
+    float vd_row[SUB];
+#pragma unroll
+    for (int z = 0; z < SUB; ++z) vd_row[z] = value_scale[z] * v_down;
 #pragma unroll
     for (int kk = 0; kk < 2 * SUB; ++kk) {
-      uint32_t p[NT][2];
+      uint32_t p[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float vd = vs[kk][e] * v_down;
-          float x, y;
-          f2_unpack(f2_sub(f2_pack(s[kk][nt][2 * e], s[kk][nt][2 * e + 1]), f2_pack(mx[nt][0], mx[nt][1])), x, y);
-          const uint64_t e2 = f2_pack(ex2(x), ex2(y));
-          sum2[nt] = f2_add(sum2[nt], e2);
-          f2_unpack(f2_mul(e2, f2_pack(vd, vd)), x, y);
-          p[nt][e] = transpose8x8(pack_f16(x, y));
-        }
+      for (int e = 0; e < 2; ++e) {
+        const float vd = __shfl_sync(0xffffffffu, vd_row[kk / 2], 16 * (kk & 1) + kr0 + e);
+        float x, y;
+        f2_unpack(f2_sub(f2_pack(s[kk][2 * e], s[kk][2 * e + 1]), f2_pack(mx[0], mx[1])), x, y);
+        const uint64_t e2 = f2_pack(ex2(x), ex2(y));
+        sum2 = f2_add(sum2, e2);
+        f2_unpack(f2_mul(e2, f2_pack(vd, vd)), x, y);
+        p[e] = transpose8x8(pack_f16(x, y));
+      }
       const uint8_t* vp = base + v_at + 16 * kk * S.bytes;
       uint32_t fa[8], fb[8];  // even and odd rows: k columns 2t.. and 2t + 8..
       value_codes<FMT>(vp + va, vp + vb, g, fa);
@@ -500,8 +494,7 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         const uint32_t frag[4] = {fa[2 * d], fa[2 * d + 1], fb[2 * d], fb[2 * d + 1]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(o[d][nt], frag, p[nt][0], p[nt][1]);
+        mma(o[d], frag, p[0], p[1]);
       }
     }
     __syncwarp();
@@ -514,45 +507,40 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
 
   // ---------------------------------------------------------------------- results
   const float up = v_top * (1.f / (1 << kVExp));
+  float sum[2];
+  f2_unpack(sum2, sum[0], sum[1]);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float sum[2];
-    f2_unpack(sum2[nt], sum[0], sum[1]);
+  for (int e = 0; e < 2; ++e) {
+    float l = group_sum(sum[e]);
+    const int k = 2 * t + e;
+    if (k >= mt) continue;
+    const long long ci = cb + k;
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float total = group_sum(sum[e]);
-      const int k = 8 * nt + 2 * t + e;
-      if (k >= mt) continue;
-      const long long ci = cb + k;
-      float x[8];
+    for (int d = 0; d < 4; ++d) {
+      x[2 * d] = o[d][e] * up;
+      x[2 * d + 1] = o[d][e + 2] * up;
+    }
+    if (w.s == 0) {  // the candidate itself
+      const float ps = ex2(self[e] - mx[e]);
+      float vf[8];
+      Elem<__nv_bfloat16>::unpack(
+          __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.v + ci * a.tok_stride + h * kQDh + 8 * g)), vf);
+      l += ps;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        x[2 * d] = o[d][nt][e] * up;
-        x[2 * d + 1] = o[d][nt][e + 2] * up;
-      }
-      float l = total;
-      if (w.s == 0) {  // the candidate itself
-        const float ps = ex2(self[nt][e] - mx[nt][e]);
-        float vf[8];
-        Elem<__nv_bfloat16>::unpack(
-            __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.v + ci * a.tok_stride + h * kQDh + 8 * g)), vf);
-        l += ps;
+      for (int d = 0; d < 8; ++d) x[d] = fmaf(ps, vf[d], x[d]);
+    }
+    if (P.part) {
+      float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kQPart;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) x[d] = fmaf(ps, vf[d], x[d]);
-      }
-      if (P.part) {
-        float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kQPart;
+      for (int d = 0; d < 8; d += 2) *reinterpret_cast<float2*>(dst + 8 * g + d) = make_float2(x[d], x[d + 1]);
+      if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(mx[e], l);
+    } else {
+      const float inv = 1.f / l;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) *reinterpret_cast<float2*>(dst + 8 * g + 2 * d) = make_float2(x[2 * d], x[2 * d + 1]);
-        if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(mx[nt][e], l);
-      } else {
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) x[d] *= inv;
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + 8 * g) =
-            Elem<__nv_bfloat16>::pack(x);
-        if (a.lse && g == 0) a.lse[(long long)h * a.T + ci] = (mx[nt][e] + log2f(l) - row_term[nt][e]) * kLn2;
-      }
+      for (int d = 0; d < 8; ++d) x[d] *= inv;
+      *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + 8 * g) = Elem<__nv_bfloat16>::pack(x);
+      if (a.lse && g == 0) a.lse[(long long)h * a.T + ci] = (mx[e] + log2f(l) - row_term[e]) * kLn2;
     }
   }
 }
@@ -608,51 +596,57 @@ __global__ void __launch_bounds__(kHeads * 32) k_qcached_join(const __grid_const
 }
 
 struct Plan {
-  int nt;  // column tiles of 8 candidates, or 0: the tensor-core form with 128 candidates an item
+  bool tc;  // the tensor-core form: items of a head and 128 candidates in place of blocks
   int groups, ctiles, splits, chunk;
   long long units;  // blocks, or items, of one range
 };
-constexpr int kTcFrom = 49;  // bound of the candidates a user from which the tensor-core form runs
+// From how many candidates a user the tensor-core form runs, and from how many rows for all blocks:
+// at 256 users x 480 rows of 8 heads it takes 109 us for anything up to 128 candidates, the blocks
+// 88 us for 32, 109 for 40, 129 for 48.  But its item is a long chain (31 us alone for 480 rows),
+// and blocks are faster while they find free SMs: 128 candidates x 480 rows 16 against 25 us for 1
+// user (7680 rows), 31 against 37 for 16 users (123 thousand), 53 against 31 for 32.
+constexpr int kTcFrom = 41;
+constexpr long long kTcRows = 1 << 17;
 
-// Blocks are one user's 8 heads and up to 32 candidates (tensor cores: items of a head and 128
-// candidates); while they do not fill the 148 SMs a few times over, the history is cut into ranges
-// of at least 64 (256) rows.
+// Blocks are one user's 8 heads and 8 candidates.  More candidates take more blocks, which read
+// the rows from L2 again: tiles of 16 and 32 candidates share the unpacking, but
+// their registers cost warps (32 candidates: 139 us in one tile, 90 us in four).
+// The history is cut into ranges where that fills the 148 SMs better.  In units of a row's time in
+// a block that has its SM to itself: a block takes its rows and about 64 to start, blocks of one
+// SM share it, and the join costs about 250.  (4 users x 65536 rows: 78 us in 37 ranges, 112 in
+// 148; 300 users x 4096 rows: 252 us uncut, 193 in 6; 128 users x 480 rows: 25 us uncut, 33 in 2.)
 Plan plan(int B, int H, int max_cand, int max_len) {
   Plan p;
-  const bool tc = max_cand >= kTcFrom;
-  p.nt = tc ? 0 : max_cand <= 8 ? 1 : max_cand <= 16 ? 2 : 4;
   p.groups = (H + kHeads - 1) / kHeads;
-  const int tile = tc ? 128 : 8 * p.nt, least = tc ? 256 : 64;
+  p.tc = max_cand >= kTcFrom &&
+         (long long)B * p.groups * ((max_cand + kCands - 1) / kCands) * max_len >= kTcRows;
+  const int tile = p.tc ? 128 : kCands, least = p.tc ? 256 : 64, slots = p.tc ? 296 : 148;
   p.ctiles = max_cand > tile ? (max_cand + tile - 1) / tile : 1;
-  p.units = (long long)B * (tc ? H : p.groups) * p.ctiles;
-  const long long want = (148 * 4 + p.units - 1) / p.units;
-  const long long most = (max_len + least - 1) / least;
-  const long long s = want < most ? want : most;
-  p.splits = s > 1 ? (int)s : 1;
-  p.chunk = ((max_len + p.splits - 1) / p.splits + 63) / 64 * 64;
-  if (p.chunk > 0) p.splits = (max_len + p.chunk - 1) / p.chunk;
-  if (p.splits < 1) p.splits = 1;
+  p.units = (long long)B * (p.tc ? H : p.groups) * p.ctiles;
+  auto rows = [&](long long s) { return (max_len + s * 64 - 1) / (s * 64) * 64; };
+  auto cost = [&](long long s) { return (p.units * s + slots - 1) / slots * (rows(s) + 64) + (s > 1 ? 250 : 0); };
+  long long best = 1;
+  for (int k = 1; k <= 16; ++k) {  // whole rounds of the SMs
+    long long s = (long long)slots * k / p.units;
+    const long long most = (max_len + least - 1) / least;
+    if (s > most) s = most;
+    if (s > 1 && cost(s) < cost(best)) best = s;
+  }
+  p.chunk = (int)rows(best);
+  p.splits = p.chunk > 0 ? (max_len + p.chunk - 1) / p.chunk : 1;
   return p;
 }
 
-template <int FMT, int NT, int SUB>
+// Tiles of 64 rows of 4 bits (156 us against 165 us with 32, at 256 users x 4096 rows) or 32 of 8
+// bits: about 100 KB of stages for each of two blocks an SM.
+template <int FMT>
 int launch(const Params& P, unsigned blocks, cudaStream_t st) {
   static DeviceOnce once;
-  constexpr int rows = kStages * 32 * SUB;
-  if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, NT, SUB>, rows * qrow(kHeads, FMT).bytes))
+  constexpr int sub = FMT == GENRANK_QCACHE_INT4 ? 2 : 1, rows = kStages * 32 * sub;
+  if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, sub>, rows * qrow(kHeads, FMT).bytes))
     return GENRANK_ERR_CUDA;
-  k_qcached<FMT, NT, SUB><<<blocks, kThreads, rows * qrow(P.c.a.H < kHeads ? P.c.a.H : kHeads, FMT).bytes, st>>>(P);
+  k_qcached<FMT, sub><<<blocks, kThreads, rows * qrow(P.c.a.H < kHeads ? P.c.a.H : kHeads, FMT).bytes, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
-}
-
-// Tiles of 64 rows of 4 bits (172 us against 190 us with 32, at 256 users x 4096 rows) or 32 of 8
-// bits, about 100 KB of stages for each of two blocks an SM; of 32 where the accumulators of more
-// than 8 candidates need the registers.
-template <int FMT>
-int launch_nt(const Params& P, int nt, unsigned blocks, cudaStream_t st) {
-  return nt == 1   ? launch<FMT, 1, FMT == GENRANK_QCACHE_INT4 ? 2 : 1>(P, blocks, st)
-         : nt == 2 ? launch<FMT, 2, 1>(P, blocks, st)
-                   : launch<FMT, 4, 1>(P, blocks, st);
 }
 
 }  // namespace qca
@@ -675,9 +669,9 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   P.chunk = p.chunk;
   P.part = p.splits > 1 ? (float*)c.a.ws : nullptr;
   const unsigned blocks = (unsigned)(p.units * p.splits);
-  const int rc = p.nt == 0 ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
-                 : c.format == GENRANK_QCACHE_INT8 ? launch_nt<GENRANK_QCACHE_INT8>(P, p.nt, blocks, st)
-                                                   : launch_nt<GENRANK_QCACHE_INT4>(P, p.nt, blocks, st);
+  const int rc = p.tc ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
+                 : c.format == GENRANK_QCACHE_INT8 ? launch<GENRANK_QCACHE_INT8>(P, blocks, st)
+                                                   : launch<GENRANK_QCACHE_INT4>(P, blocks, st);
   if (rc != GENRANK_OK || p.splits == 1) return rc;
   k_qcached_join<<<(unsigned)joins, kHeads * 32, 0, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;

@@ -376,6 +376,11 @@ def _device_of(what, t):
     return dev
 
 
+def _stream_of(dev, stream):
+    """The raw handle of `stream`, or of device dev's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _vec(what, name, t, dev, dtype, least):
     """The address of a contiguous tensor of at least `least` elements on device dev."""
     if t.dtype is not dtype or t.get_device() != dev or t.numel() < least or not t.is_contiguous():
@@ -438,7 +443,7 @@ def qcache_append(src_offsets, src_len, k, v, tok_stride, H, dh, pos, ts, cache,
         _vec(what, "pos", pos, dev, torch.int32, T), _vec(what, "ts", ts, dev, torch.int64, T),
         int(fmt), _cache(what, cache, dev, H, dh, fmt), cache.shape[0],
         _vec(what, "rows", rows, dev, torch.int64, B),
-        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream(stream))
+        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream_of(dev, stream))
     _check(rc, "genrank_qcache_append")
 
 
@@ -459,7 +464,7 @@ def qcache_read(dst_offsets, dst_len, cache, rows, k, v, tok_stride, H, dh, pos,
         _mat(what, "v", v, dev, dt, T, tok_stride, H * dh), int(tok_stride), _dtype_code(k),
         None if pos is None else _vec(what, "pos", pos, dev, torch.int32, T),
         None if ts is None else _vec(what, "ts", ts, dev, torch.int64, T),
-        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream(stream))
+        _vec(what, "dev_err", dev_err, dev, torch.int32, 1), _stream_of(dev, stream))
     _check(rc, "genrank_qcache_read")
 
 
@@ -494,7 +499,7 @@ def attn_fwd_qcached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, cache, 
         None if lse is None else _vec(what, "lse", lse, dev, torch.float32, H * C),
         None if ws is None else _vec(what, "ws", ws, dev, torch.uint8, 0),
         0 if ws is None else ws.numel(), _vec(what, "dev_err", dev_err, dev, torch.int32, 1),
-        _stream(stream))
+        _stream_of(dev, stream))
     _check(rc, "genrank_attn_fwd_qcached")
 
 
