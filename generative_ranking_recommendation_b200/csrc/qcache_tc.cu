@@ -94,6 +94,13 @@ constexpr uint32_t kIdescS = idesc_f16(BM, BN, 0);
 constexpr uint32_t kIdescBias = idesc_bf16_f32(BM, BN, 0, 0);
 constexpr uint32_t kIdescPV = idesc_f16(BM, kQDh, 1);
 
+// Operands are codes times their scale over the item's largest, times 2^kUp: as high in fp16's range
+// as the constants of the unpacking allow (72 f and 1152 f below 65504), so that a row whose scale is
+// far below the largest keeps its bits down to 2^-25 (4 bits) or 2^-30 (8 bits) of it.
+template <int FMT>
+constexpr int kUp = FMT == GENRANK_QCACHE_INT4 ? 9 : 6;
+constexpr float kPastEnd = -0x1p100f;  // column term of a key past the end: exact in bf16, and with
+constexpr int kMinUp = -24;            // the candidate's 2^24 at most finite
 constexpr float kPExp = 6.f;        // P holds 2^(x - max + 6)
 constexpr float kMaxSum = 65504.f;  // a tile's sum up to this leaves no term beyond fp16
 
@@ -111,7 +118,7 @@ struct Item {
   int h, s, cb, mt;      // head, range, first candidate row, candidates (at most 128)
   int n, rows, tiles;    // the user's rows, the item's, and their tiles (-1: no more items)
   int at;                // the item's first cache row
-  int ke, ve;            // powers of two above every K and V scale
+  int ke, ve;            // powers of two, 2^kUp of which are above every K and V scale
   long long t_ref;       // time of the user's first candidate, the origin of the bias
   long long t_min;       // earliest time of the item's candidates
   int c0, pad;
@@ -123,6 +130,7 @@ GR_DEVICE int exp_above(float x) { return min(max((int)(__float_as_uint(x) >> 23
 
 // The block's next item with something to do, from index w on (w moves past it), by a full warp.
 // Users whose layout is broken are flagged and left out.
+template <int FMT>
 GR_DEVICE Item next_item(const Params& P, const QRow& L, unsigned& w) {
   const QcachedAttnArgs& c = P.c;
   const int lane = threadIdx.x & 31;
@@ -176,8 +184,8 @@ GR_DEVICE Item next_item(const Params& P, const QRow& L, unsigned& w) {
       vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
       it.t_min = min(it.t_min, __shfl_xor_sync(0xffffffffu, it.t_min, o));
     }
-    it.ke = exp_above(kmax);
-    it.ve = exp_above(vmax);
+    it.ke = max(exp_above(kmax) - kUp<FMT>, -126);
+    it.ve = max(exp_above(vmax) - kUp<FMT>, -126);
     break;
   }
   return it;
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       if (j == min(cur.tiles, R::kSlots)) {
         // the next item's record, and the load of its Q rows, while this one's first tiles are
         // worked on
-        nx = next_item(P, L, w);
+        nx = next_item<FMT>(P, L, w);
         const int rs = qi % kRecs, qb = qi & 1;
         ok = wait_warp(&bars[kRecEmpty + rs], par(qi / kRecs) ^ 1u, abort_flag) &&
              (nx.tiles < 0 || wait_warp(&bars[kQEmpty + qb], par(qi >> 1) ^ 1u, abort_flag));
@@ -485,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           bad_time |= on && tj > t_min;
           bad_pos |= on && (tail.z < 0 || tail.z > n1);
           const float dp = (float)min(tail.z - n1, 0), dt = (float)min(tj - t_ref, 0ll);
-          // a key past the end scores -1e30 scale log2 e, far below any other
-          term4 = bf16_parts(on ? fmaf(sp2, dp, st2 * dt) * inv_sl2 : -1e30f);
+          term4 = bf16_parts(on ? fmaf(sp2, dp, st2 * dt) * inv_sl2 : kPastEnd);
         }
         // (a K buffer is free after its S, long before the V buffer of the same tile)
         if (!wait_warp(&bars[(side == 0 ? kKEmpty : kVEmpty) + st], par(g / kStages) ^ 1u, abort_flag)) {
@@ -613,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
 #pragma unroll
               for (int e = 0; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
             }
-            mx = mx * f - kPExp;
+            mx = __fmaf_ru(mx, f, -kPExp);  // up: no x - m is above kPExp, however coarse floats are there
             if (j == 0) {
               m = mx > -INFINITY ? mx : 0.f;
             } else {
@@ -734,9 +741,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        // q = q' 2^qe; where scores are below 2^-100 of a unit, q' vanishes instead
+        // q = q' 2^qe, q' below 2 (and smaller where all scores are: its 2^-25 then stands for
+        // 2^-43 of a score)
         int qe = min(max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -126), 126);
-        qe = max(qe, -100 - nx.ke);
+        qe = max(qe, min(kMinUp - nx.ke, 126));
         const int up = min(qe + nx.ke, 126);
         const float qd = pow2(-qe);
         float f[8];  // (rows past the item's candidates are never written out)

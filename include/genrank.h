@@ -338,7 +338,7 @@ size_t genrank_attn_cached_workspace_size(int B, int64_t C, int64_t Th, int H, i
  *   [ts int64][pos int32][0 int32][zeros to an odd multiple of 16 bytes]
  * cb = 64 (int8: one byte c + 128 per value) or 32 (int4: one nibble c + 8 per value, the
  * low nibble first).  User u's rows are rows[u], rows[u] + 1, ... (a device array), one per
- * history token, oldest first; the rest of the cache is not read, and never written.
+ * history token, oldest first; what the rest of the cache holds does not matter, and it is never written.
  * Rows of R or offsets beyond 2^31 bytes are fine. */
 enum { GENRANK_QCACHE_INT8 = 0, GENRANK_QCACHE_INT4 = 1 };
 
@@ -388,7 +388,11 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  * GENRANK_DERR_LAYOUT (a user's offsets or rows outside their arrays: the user is left out;
  * more than max_cand candidates or max_len rows: the rest is left out), GENRANK_DERR_TS_ORDER
  * (a cached time after a candidate's), GENRANK_DERR_POS_RANGE (a cached position outside
- * [0, n_u + 1]); in the last two cases the distance counts as zero. */
+ * [0, n_u + 1]); in the last two cases a distance below zero (in time: from the user's first
+ * candidate) counts as zero.
+ * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, a head scaled
+ * by a power of two: exact down to 2^-17 of its largest element, 2^-25 of that below; softmax
+ * weights are rounded to fp16's 11 bits. */
 int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t *cand_offsets, int max_cand,
                              const void *q_c, const void *k_c, const void *v_c,
                              int64_t cand_stride, const void *cache, int64_t R,

@@ -457,6 +457,189 @@ def test_nan_and_infinity_stay_in_their_rows(G, bits):
     assert np.array_equal(o[keep], clean[keep])
 
 
+# ------------------------------------------------------------------------------------------
+# attention for many candidates: the kernel is chosen by the bounds of candidates and rows, so
+# loose bounds (which the call allows) bring any batch to it
+# ------------------------------------------------------------------------------------------
+
+WIDE = dict(max_cand=1200, max_len=4096)
+# lengths around the tile of 64 rows, candidates around the tile of 128
+TILES = [(0, 130), (1, 1), (63, 127), (64, 128), (65, 129), (0, 0), (128, 0), (129, 300), (480, 41), (300, 257), (0, 1)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("H", [1, 3, 8, 17])
+def test_many_candidates(G, bits, H):
+    _check(G, *_batch(30 + H, TILES, H, bits, tc_spread=5000), extra=3, **WIDE)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("users", [SMALL, LARGE], ids=["small", "large"])
+def test_few_candidates_within_loose_bounds(G, bits, users):
+    _check(G, *_batch(40, users, 5, bits, tc_spread=5000), extra=1, lse=False, **WIDE)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("m", [40, 41])
+def test_both_sides_of_the_choice(G, bits, m):
+    _check(G, *_batch(41, [(480, m)] * 60, 2, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("users,H,bounds", [([(5000, 130)], 2, dict(max_cand=600)), ([(3000, 70), (0, 50), (700, 200)], 1, dict(max_cand=900)),
+                                            ([(4097, 45)] * 3, 3, dict(max_cand=128))])
+def test_many_candidates_in_ranges(G, bits, users, H, bounds):
+    batch, values = _batch(42, users, H, bits)
+    assert G.attn_qcached_workspace_size(len(users), len(batch["tc"]), H, 64, bounds["max_cand"], max(n for n, _ in users)) > 0
+    _check(G, batch, values, extra=2, **bounds)
+
+
+def test_more_items_than_blocks(G):
+    """Every block walks over several items of unequal length, empty ones among them."""
+    r = np.random.default_rng(43)
+    users = [(int(r.integers(0, 200)), int(r.integers(0, 90))) for _ in range(150)]
+    for bits in (8, 4):
+        _check(G, *_batch(43, users, 4, bits), max_cand=128, max_len=1000)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_unequal_magnitudes_of_many_candidates(G, bits):
+    """As test_unequal_magnitudes: the most recent tile is far from the maximum, in either direction."""
+    batch, values = _batch(44, [(200, 60), (333, 130), (70, 3)], 4, bits, spread=10.0, qscale=1e-3)
+    _check(G, batch, values, **WIDE)
+    batch, values = _batch(45, [(200, 60), (333, 130), (70, 3)], 4, bits, qscale=60.0)
+    batch["qkv"][1, ::3] *= 8.0
+    batch["qkv"][1, 1::3] *= -8.0
+    _check(G, batch, values, **WIDE)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_small_values_outweigh_large_ones(G, bits):
+    """Rows whose value scale is 2^-20 of the largest hold all the weight: they keep their bits."""
+    H = 2
+    batch, _ = _batch(46, [(150, 50)], H, bits, qscale=0.25)
+    r, R = np.random.default_rng(46), len(batch["cache"])
+    k, v = _kv(r, R, H), _kv(r, R, H)
+    pos, ts = np.zeros(R, np.int64), np.zeros(R, np.int64)
+    at = int(batch["rows"][0])
+    pos[at:at + 150], ts[at:at + 150] = np.arange(1, 151), batch["tc"][0] - 9
+    v[at:at + 150] *= np.float32(2.0 ** -20)
+    v[at + 20] *= np.float32(2.0 ** 20)
+    pos[at + 20] = 0
+    batch["qkv"][2] *= np.float32(2.0 ** -20)
+    batch["cache"] = oracle.qcache_rows(k, v, pos, ts, bits)
+    for kw in (WIDE, {}):
+        # the large row is left a weight below 2^-80 by its position
+        _check(G, batch, (oracle.qcache_values(k, bits), oracle.qcache_values(v, bits), pos, ts), slopes=([0.5, 1.0], [0.0, 0.0]), **kw)
+
+
+def test_extreme_magnitudes_of_many_candidates(G):
+    """As test_extreme_magnitudes_of_q, with a zero and a tiny candidate among the others."""
+    for up in (100, -100):
+        for bits in (8, 4):
+            batch, _ = _batch(47, [(77, 60)], 2, bits)
+            r, n, R = np.random.default_rng(1), 77, len(batch["cache"])
+            k, v = _kv(r, R, 2) * np.float32(2.0 ** -up), _kv(r, R, 2)
+            pos, ts = np.zeros(R, np.int64), np.zeros(R, np.int64)
+            s = slice(batch["rows"][0], batch["rows"][0] + n)
+            pos[s], ts[s] = np.arange(1, n + 1), batch["tc"][0] - 5
+            batch["cache"] = oracle.qcache_rows(k, v, pos, ts, bits)
+            batch["qkv"][0] *= np.float32(2.0 ** up)
+            batch["qkv"][0, 1] = 0.0
+            batch["qkv"][0, 2] *= np.float32(2.0 ** -12)
+            batch["qkv"][0, 3] *= np.float32(2.0 ** -80 if up > 0 else 2.0 ** -20)
+            batch["qkv"][1] *= np.float32(2.0 ** -up)
+            _check(G, batch, (oracle.qcache_values(k, bits), oracle.qcache_values(v, bits), pos, ts), **WIDE)
+    batch, values = _batch(48, [(77, 60)], 2, 4)
+    batch["qkv"][0] = 0.0  # every score is the bias, a user's keys are zero as well
+    _check(G, batch, values, **WIDE)
+
+
+@pytest.mark.parametrize("kw", [WIDE, {}], ids=["wide", "exact"])
+def test_scores_beyond_floats_whole_numbers(G, kw):
+    """Slopes that take every cached score to -1e9 and below, where neighbouring floats are 64 and
+    more apart: the candidates' own scores hold all the weight, and nothing overflows."""
+    for slopes in (([0.1, 0.0], [1.0, 30.0]), ([1e7, 1e8], [0.0, 0.0])):
+        batch, values = _batch(49, [(300, 50), (64, 3)], 2, 4, qscale=8.0)
+        k, v, pos, ts = values
+        ts[ts > 0] -= 1 << 30
+        batch["cache"] = oracle.qcache_rows(k, v, pos, ts, 4)
+        o, _, _ = _check(G, batch, values, slopes=slopes, **kw)
+        assert np.array_equal(o, batch["qkv"][2].astype(np.float64))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_nan_and_infinity_stay_in_their_rows_of_many_candidates(G, bits):
+    batch, values = _batch(50, [(140, 60), (140, 60)], 4, bits)
+    b = batch
+
+    def run(cache, qkv):
+        return _score(G, qkv, b["coff"], _dev(cache), b["rows"], b["lens"], b["tc"], 4, bits, **WIDE)
+
+    clean, _, code = run(b["cache"], b["qkv"])
+    assert code == 0 and np.isfinite(clean).all()
+    for side in (0, 1):
+        k, v, pos, ts = (x.copy() for x in values)
+        at = b["rows"][0] + 70
+        (k if side == 0 else v)[at, 1, 3] = np.nan
+        rb = b["cache"].copy()
+        rb[at] = oracle.qcache_rows(k[at:at + 1], v[at:at + 1], pos[at:at + 1], ts[at:at + 1], bits)
+        o, lse, code = run(rb, b["qkv"])
+        assert code == 0
+        assert np.isnan(o[:60, 1]).all() and np.array_equal(np.isnan(lse[:, :60]).any(1), [False, side == 0, False, False])
+        keep = np.ones(o.shape[:2], bool)
+        keep[:60, 1] = False
+        assert np.array_equal(o[keep], clean[keep])
+    qkv = b["qkv"].copy()
+    qkv[0, 2, 0, 5] = np.nan
+    qkv[1, 4, 1, 6] = np.nan
+    qkv[2, 6, 2, 7] = np.nan
+    qkv[0, 8, 3, 7] = np.inf
+    qkv[0, 61, 3, 7] = -np.inf
+    o, lse, code = run(b["cache"], qkv)
+    assert code == 0
+    assert np.isnan(o[2, 0]).all() and np.isnan(o[4, 1]).all() and np.isnan(o[8, 3]).all() and np.isnan(o[61, 3]).all()
+    assert np.isnan(o[6, 2, 7]) and np.isnan(lse[:, 6]).sum() == 0
+    keep = np.ones(o.shape[:2], bool)
+    keep[[2, 4, 6, 8, 61], [0, 1, 2, 3, 3]] = False
+    assert np.array_equal(o[keep], clean[keep])
+
+
+def test_errors_of_many_candidates(G):
+    batch, values = _batch(51, [(140, 50), (133, 60), (70, 50)], 2, 4, order=[0, 1, 2])
+    b = {k: (list(v) if k in ("rows", "lens") else v) for k, v in batch.items()}
+    cache = _dev(b["cache"])
+    R = len(b["cache"])
+
+    def run(max_cand=1200, max_len=4096, **kw):
+        a = {**b, **kw}
+        return _score(G, a["qkv"], a["coff"], cache, a["rows"], a["lens"], a["tc"], 2, 4, max_cand=max_cand, max_len=max_len)
+
+    clean, _, code = run()
+    assert code == 0
+    left = np.ones(160, bool)
+    left[50:110] = False
+    for kw in (dict(rows=[b["rows"][0], R - 5, b["rows"][2]]), dict(rows=[b["rows"][0], -1, b["rows"][2]]),
+               dict(lens=[140, -1, 70])):
+        o, lse, code = run(**kw)
+        assert code == G.DERR["LAYOUT"]
+        assert np.isnan(o[50:110]).all() and np.array_equal(o[left], clean[left])
+    assert run(coff=np.array([0, 50, 110, 170]))[2] == G.DERR["LAYOUT"]
+    o, _, code = run(max_cand=55, max_len=8192)  # the second user's last five are left out
+    assert code == G.DERR["LAYOUT"] and np.isnan(o[105:110]).all()
+    assert np.array_equal(np.delete(o, range(105, 110), 0), np.delete(clean, range(105, 110), 0))
+    assert run(max_len=139)[2] == G.DERR["LAYOUT"]
+    tc = b["tc"].copy()
+    tc[70] -= 1 << 30
+    o, _, code = run(tc=tc)
+    assert code == G.DERR["TS_ORDER"] and np.array_equal(o[:50], clean[:50])
+    k, v, pos, ts = values
+    pos[b["rows"][2] + 3] = 200
+    cache = _dev(oracle.qcache_rows(k, v, pos, ts, 4))
+    o, _, code = run()
+    assert code == G.DERR["POS_RANGE"] and np.array_equal(o[:110], clean[:110])
+
+
 def test_attention_layout_and_order_errors(G):
     batch, values = _batch(18, [(40, 2), (33, 3), (20, 2)], 2, 4, order=[0, 1, 2])
     b = {k: (list(v) if k in ("rows", "lens") else v) for k, v in batch.items()}
@@ -563,10 +746,11 @@ def test_a_server_s_run(G, bits):
 
 
 def test_streams_and_graphs(G):
-    """Calls on a side stream; two captured graphs (a joined and a direct one) replayed in turn on
+    """Calls on a side stream; captured graphs (joined and direct ones, few candidates and many) replayed in turn on
     changed inputs, bit for bit the eager results."""
-    cases = [_batch(22, [(700, 2)], 8, 4), _batch(23, [(50, 3)] * 200, 8, 8)]
-    H, d, fmts = 8, 512, [G.QCACHE_INT4, G.QCACHE_INT8]
+    cases = [_batch(22, [(700, 2)], 8, 4), _batch(23, [(50, 3)] * 200, 8, 8), _batch(24, [(3000, 60)] * 2, 8, 4),
+             _batch(25, [(500, 50)] * 50, 8, 8)]
+    H, d, fmts = 8, 512, [G.QCACHE_INT4, G.QCACHE_INT8] * 2
     sp, st = G.alibi_slopes(H)
     calls = []
     for (b, _), fmt in zip(cases, fmts):
