@@ -32,4 +32,11 @@ __host__ __device__ constexpr QRow qrow(int H, int format) {
   return r;
 }
 
+#ifdef __CUDACC__
+// A kernel launched to follow another early (programmatic stream serialisation) starts once every
+// block of that one has called grid_release or ended, and waits in grid_wait for its end and results.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 }  // namespace gr

@@ -28,7 +28,7 @@
 //   * Short of blocks, the history is cut into ranges; the ranges' (max, sum, O) in fp32 are
 //     joined by a second kernel, always in the same order.
 // Bound: with one candidate the copies, at 256 users x 4096 rows of 8 heads 156 us for int4 rows
-// (587 MB, 3.8 TB/s; the copies alone take 117) and 211 us for int8 (1124 MB, 5.3 TB/s); with more
+// (587 MB, 3.8 TB/s; the copies alone take 117) and 199 us for int8 (1124 MB, 5.7 TB/s); with more
 // the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 88 us).
 #include <cuda_fp16.h>
 
@@ -54,6 +54,7 @@ struct Params {
   int ctiles;  // candidate tiles of a user
   int splits;  // ranges of the history
   int chunk;   // rows of a range, a multiple of 64
+  int ways;    // half-warps that join a candidate's ranges
   float* part;  // [splits][C][H][kQPart], or null: one range, written in place
 };
 
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   volatile int* abort_flag = &abort_word;
   const QcachedAttnArgs& c = P.c;
   const AttnArgs& a = c.a;
+  grid_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Work w = work_of(P, blockIdx.x);
   int c0, m, n;
@@ -545,54 +547,78 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   }
 }
 
-// Joins the ranges of a user's candidate: a warp per (candidate, head), two ranges at a time,
-// four dimensions a lane.  The order of the sums depends on the number of ranges alone.
-__global__ void __launch_bounds__(kHeads * 32) k_qcached_join(const __grid_constant__ Params P) {
+// Joins the ranges of a candidate and head: `ways` half-warps, four dimensions a lane, each take
+// every ways-th range, then the first adds up what they found.  The order of the sums depends on the
+// number of ranges alone.  What it takes is latency (4 users' 8 candidates of 8 heads in 37 ranges,
+// 2.5 MB), so it is launched while the ranges are worked on and loads four of them at once.
+constexpr int kHalfWarps = 16;
+__global__ void __launch_bounds__(kHalfWarps * 16) k_qcached_join(const __grid_constant__ Params P) {
+  __shared__ __align__(16) float parts[kHalfWarps][kQDh];
+  __shared__ float2 stats[kHalfWarps];  // maximum and sum
   const AttnArgs& a = P.c.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned b = blockIdx.x;
-  const int k = b % P.c.max_cand;
-  b /= P.c.max_cand;
-  const int g = b % P.groups, u = b / P.groups;
-  int c0, m, n;
+  const int hw = threadIdx.x >> 4, lane = threadIdx.x & 15, d = 4 * lane;
+  const int way = hw & (P.ways - 1);
+  unsigned i = blockIdx.x * (unsigned)(kHalfWarps / P.ways) + hw / P.ways;
+  const int h = i % (unsigned)a.H;
+  i /= (unsigned)a.H;
+  const int k = i % (unsigned)P.c.max_cand, u = i / (unsigned)P.c.max_cand;
+  int c0 = 0, m = 0, n = 0;
   long long at;
-  if (!user_of(P.c, u, c0, m, at, n)) return;
-  m = min(m, P.c.max_cand);
-  n = min(n, P.c.max_len);
-  const int h = g * kHeads + warp;
-  if (h >= a.H || k >= m) return;
-  const int splits = min(P.splits, max(1, (n + P.chunk - 1) / max(1, P.chunk)));
+  const bool on = u < a.B && user_of(P.c, u, c0, m, at, n) && k < m;
+  const int splits = on ? min(P.splits, max(1, (min(n, P.c.max_len) + P.chunk - 1) / P.chunk)) : 0;
   const long long ci = c0 + k;
+  const float row_term = on && a.lse ? a.slope_time[h] * kLog2e * (float)(a.ts[ci] - a.ts[c0]) : 0.f;
+  grid_wait();  // the ranges are there
+
   const float* src = P.part + (ci * a.H + h) * kQPart;
   const long long step = a.T * a.H * kQPart;
-  const int half = lane >> 4, d = 4 * (lane & 15);
-  float top = -INFINITY;
-  for (int s = lane; s < splits; s += 32) top = fmaxf(top, src[s * step + kQDh]);
+  float top = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = way; s < splits; s += 4 * P.ways) {
+    float2 ml[4], lo[4], hi[4];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = half; s < splits; s += 2) {
-    const float* p = src + s * step;
-    const float2 ml = *reinterpret_cast<const float2*>(p + kQDh);
-    const float2 v0 = *reinterpret_cast<const float2*>(p + d), v1 = *reinterpret_cast<const float2*>(p + d + 2);
-    const float f = ex2(ml.x - top);
-    l = fmaf(ml.y, f, l);
-    x[0] = fmaf(v0.x, f, x[0]);
-    x[1] = fmaf(v0.y, f, x[1]);
-    x[2] = fmaf(v1.x, f, x[2]);
-    x[3] = fmaf(v1.y, f, x[3]);
-  }
-  l += __shfl_xor_sync(0xffffffffu, l, 16);
+    for (int j = 0; j < 4; ++j) {
+      const float* p = src + (s + j * P.ways) * step;
+      const bool there = s + j * P.ways < splits;
+      ml[j] = there ? *reinterpret_cast<const float2*>(p + kQDh) : make_float2(-INFINITY, 0.f);
+      lo[j] = there ? *reinterpret_cast<const float2*>(p + d) : make_float2(0.f, 0.f);
+      hi[j] = there ? *reinterpret_cast<const float2*>(p + d + 2) : make_float2(0.f, 0.f);
+    }
+    const float next = fmaxf(top, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+    const float al = ex2(top - next);
+    top = next;
+    l *= al;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = (x[i] + __shfl_xor_sync(0xffffffffu, x[i], 16)) / l;
-  if (half == 0)
-    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + d) =
-        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-  if (a.lse && lane == 0) {
-    const float rt = a.slope_time[h] * kLog2e * (float)(a.ts[ci] - a.ts[c0]);
-    a.lse[(long long)h * a.T + ci] = (top + log2f(l) - rt) * kLn2;
+    for (int e = 0; e < 4; ++e) x[e] *= al;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = ex2(ml[j].x - top);
+      l = fmaf(ml[j].y, f, l);
+      x[0] = fmaf(lo[j].x, f, x[0]);
+      x[1] = fmaf(lo[j].y, f, x[1]);
+      x[2] = fmaf(hi[j].x, f, x[2]);
+      x[3] = fmaf(hi[j].y, f, x[3]);
+    }
   }
+  *reinterpret_cast<float4*>(&parts[hw][d]) = make_float4(x[0], x[1], x[2], x[3]);
+  if (lane == 0) stats[hw] = make_float2(top, l);
+  __syncthreads();
+  if (way > 0 || !on) return;
+  const int ways = min(P.ways, splits);
+  for (int w = 1; w < ways; ++w) top = fmaxf(top, stats[hw + w].x);
+  l = x[0] = x[1] = x[2] = x[3] = 0.f;
+  for (int w = 0; w < ways; ++w) {
+    const float f = ex2(stats[hw + w].x - top);
+    const float4 v = *reinterpret_cast<const float4*>(&parts[hw + w][d]);
+    l = fmaf(stats[hw + w].y, f, l);
+    x[0] = fmaf(v.x, f, x[0]);
+    x[1] = fmaf(v.y, f, x[1]);
+    x[2] = fmaf(v.z, f, x[2]);
+    x[3] = fmaf(v.w, f, x[3]);
+  }
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + d) =
+      make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+  if (a.lse && lane == 0) a.lse[(long long)h * a.T + ci] = (top + log2f(l) - row_term) * kLn2;
 }
 
 struct Plan {
@@ -612,9 +638,10 @@ constexpr long long kTcRows = 1 << 17;
 // the rows from L2 again: tiles of 16 and 32 candidates share the unpacking, but
 // their registers cost warps (32 candidates: 139 us in one tile, 90 us in four).
 // The history is cut into ranges where that fills the 148 SMs better.  In units of a row's time in
-// a block that has its SM to itself: a block takes its rows and about 64 to start, blocks of one
-// SM share it, and the join costs about 250.  (4 users x 65536 rows: 78 us in 37 ranges, 112 in
-// 148; 300 users x 4096 rows: 252 us uncut, 193 in 6; 128 users x 480 rows: 25 us uncut, 33 in 2.)
+// one of the blocks that share an SM: a block takes its rows and about 100 to start, one that has
+// its SM to itself an eighth longer, and the join costs about 100.  (4 users x 65536 rows of 8 bits:
+// 72 us in 37 ranges, 99 in 18, 103 in 148; 64 users x 4096: 109 us uncut, 69 in 2, 59 in 4, 71 in
+// 16; 128 users x 480: 25 us uncut, 30 in 2.)
 Plan plan(int B, int H, int max_cand, int max_len) {
   Plan p;
   p.groups = (H + kHeads - 1) / kHeads;
@@ -624,7 +651,10 @@ Plan plan(int B, int H, int max_cand, int max_len) {
   p.ctiles = max_cand > tile ? (max_cand + tile - 1) / tile : 1;
   p.units = (long long)B * (p.tc ? H : p.groups) * p.ctiles;
   auto rows = [&](long long s) { return (max_len + s * 64 - 1) / (s * 64) * 64; };
-  auto cost = [&](long long s) { return (p.units * s + slots - 1) / slots * (rows(s) + 64) + (s > 1 ? 250 : 0); };
+  auto cost = [&](long long s) {
+    const long long rounds = (p.units * s + slots - 1) / slots, time = rounds * (rows(s) + 100);
+    return time + (!p.tc && rounds == 1 ? time / 8 : 0) + (s > 1 ? 100 : 0);
+  };
   long long best = 1;
   for (int k = 1; k <= 16; ++k) {  // whole rounds of the SMs
     long long s = (long long)slots * k / p.units;
@@ -659,22 +689,35 @@ size_t attn_fwd_qcached_workspace(int B, long long C, int H, int max_cand, int m
 int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   using namespace qca;
   const Plan p = plan(c.a.B, c.a.H, c.max_cand, c.max_len);
-  const long long joins = (long long)c.a.B * p.groups * c.max_cand;
-  if (p.units * p.splits > INT32_MAX || joins > INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  int ways = 2;
+  while (ways < kHalfWarps && 2 * ways < p.splits) ways *= 2;
+  const int pairs = kHalfWarps / ways;  // (candidate, head) of a block
+  const long long joins = ((long long)c.a.B * c.max_cand * c.a.H + pairs - 1) / pairs;
+  if (p.units * p.splits > INT32_MAX || (p.splits > 1 && joins * pairs > INT32_MAX)) return GENRANK_ERR_UNSUPPORTED;
   Params P;
   P.c = c;
   P.groups = p.groups;
   P.ctiles = p.ctiles;
   P.splits = p.splits;
   P.chunk = p.chunk;
+  P.ways = ways;
   P.part = p.splits > 1 ? (float*)c.a.ws : nullptr;
   const unsigned blocks = (unsigned)(p.units * p.splits);
   const int rc = p.tc ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
                  : c.format == GENRANK_QCACHE_INT8 ? launch<GENRANK_QCACHE_INT8>(P, blocks, st)
                                                    : launch<GENRANK_QCACHE_INT4>(P, blocks, st);
-  if (rc != GENRANK_OK || p.splits == 1) return rc;
-  k_qcached_join<<<(unsigned)joins, kHeads * 32, 0, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
+  if (rc != GENRANK_OK || p.splits == 1 || joins == 0) return rc;
+  // launched as soon as every block of the ranges has begun, it waits for them (grid_wait)
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)joins);
+  cfg.blockDim = dim3(kHalfWarps * 16);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_qcached_join, P) == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
 }
 
 }  // namespace gr
