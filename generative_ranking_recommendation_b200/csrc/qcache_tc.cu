@@ -193,8 +193,8 @@ GR_DEVICE Item next_item(const Params& P, const QRow& L, unsigned& w) {
 
 GR_DEVICE uint32_t par(int use) { return (uint32_t)(use & 1); }
 // Waits by a whole warp for the phase of the given parity, in few instructions (the code of 14
-// warps' roles shares the instruction cache): up to 2 million tries, each of which the hardware
-// suspends for a while, after which, or once another role has given up, it gives up.
+// warps' roles shares the instruction cache): up to 2 million tries that the hardware suspends for
+// a microsecond each, after which, or once another role has given up, it gives up.
 GR_DEVICE bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const uint32_t addr = smem_u32(bar);
 #pragma unroll 1
@@ -202,7 +202,7 @@ GR_DEVICE bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_fla
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 1000;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(addr), "r"(parity)
@@ -691,6 +691,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       if (!ok) break;
       rd[0] = m;
       rd[3 * BM] = l;
+      // the item before this one is complete: a warp that is early (an item without tiles, or of
+      // one) does not count twice for it
+      if (qi > 1 && !wait_warp(&bars[kOFull], par(qi - 2), abort_flag)) break;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars[kOFull]);

@@ -502,6 +502,20 @@ def test_more_items_than_blocks(G):
         _check(G, *_batch(43, users, 4, bits), max_cand=128, max_len=1000)
 
 
+def test_short_items_in_a_row(G):
+    """Blocks walk over a dozen items each of no tile, one or two, and few or many candidates, whose
+    roles' warps take different time."""
+    r = np.random.default_rng(52)
+    users = [(int(r.choice([0, 0, 1, 64, 64, 65, 150])), int(r.choice([1, 20, 33, 70, 100]))) for _ in range(700)]
+    for bits in (8, 4):
+        batch, values = _batch(52, users, 5, bits)
+        first = _check(G, batch, values, max_cand=128, max_len=300)
+        for _ in range(20):
+            b = dict(batch)
+            again = _score(G, b["qkv"], b["coff"], _dev(b["cache"]), b["rows"], b["lens"], b["tc"], 5, bits, max_cand=128, max_len=300)
+            assert again[2] == 0 and np.array_equal(again[0], first[0]) and np.array_equal(again[1], first[1])
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 def test_unequal_magnitudes_of_many_candidates(G, bits):
     """As test_unequal_magnitudes: the most recent tile is far from the maximum, in either direction."""
