@@ -591,10 +591,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       const Item* rec = take(qi);
       if (!rec) break;
       const int qb = qi & 1, tiles = rec->tiles;
+      const int mt = __shfl_sync(0xffffffffu, rec->mt, 0);
+      const bool idle = warp * 32 >= mt;  // none of the item's candidates
       give_back(qi);
       if (!wait_warp(&bars[kQFull + qb], par(qi >> 1), abort_flag)) break;
       float* rd = rowdata + qb * 4 * BM + r;
-      const float f = rd[0];  // x = S f
+      const float f = r < mt ? rd[0] : 0.f;  // x = S f (a row past the candidates moves nothing)
       ++qi;
       float m = 0.f, l = 0.f;
       const uint64_t f2 = f2_pack(f, f);
@@ -608,8 +610,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         }
         tc_fence_after();
         const uint32_t s_addr = lane_base + kColS + sb * BN, p_addr = lane_base + kColP + sb * (BN / 2);
+        if (idle) {  // (whatever P holds there reaches those rows of O alone)
+          if (lane == 0) mbar_arrive(&bars[kPFull + sb]);
+          continue;
+        }
         bool move = j == 0;  // the offset is set from this tile's maximum
-        for (;;) {
+        for (int pass = 0;; ++pass) {
           if (__any_sync(0xffffffffu, move)) {
             // every lane takes part in the .sync.aligned accesses; only rows that move change m
             float mx = -INFINITY;
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           f2_unpack(sum2[0], s0, s1);
           f2_unpack(sum2[1], s2, s3);
           const float rs = (s0 + s1) + (s2 + s3);
-          move = j > 0 && rs > kMaxSum;  // (a NaN stays one whatever the offset)
+          move = j > 0 && pass == 0 && rs > kMaxSum;  // (once is enough: then every term is 2^kPExp at most)
           if (!__any_sync(0xffffffffu, move)) {
             l += rs;
             break;
@@ -719,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       };
       uint4 k_next[2] = {load_k(0), load_k(1)};
       if (!wait_warp(&bars[kQRaw + qb], par(qi >> 1), abort_flag)) return false;
+      const int rows4 = (nx.mt - 32 * w4 + 3) >> 2;  // rows of candidates, by fours
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < min(rows4, 8); ++i) {
         const uint4 k4 = k_next[0];
         k_next[0] = k_next[1];
         if (i + 2 < 8) k_next[1] = load_k(i + 2);
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         qe = max(qe, min(kMinUp - nx.ke, 126));
         const int up = min(qe + nx.ke, 126);
         const float qd = pow2(-qe);
-        float f[8];  // (rows past the item's candidates are never written out)
+        float f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f2_unpack(f2_mul(f2[e], f2_pack(qd, qd)), f[2 * e], f[2 * e + 1]);
         *place = FMT == GENRANK_QCACHE_INT4
@@ -811,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       const uint64_t wo2 = f2_pack(wo, wo), wb2 = f2_pack(wb, wb);
       float* part = P.part ? P.part + (((long long)it.s * a.T + ci) * a.H + it.h) * kQPart : nullptr;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kQDh; c0 += 16) {
+      for (int c0 = 0; c0 < (32 * w4 < it.mt ? kQDh : 0); c0 += 16) {
         uint32_t o[16];
         tmem_ld16_async(lane_base + kColO + c0, o);
         tmem_ld_wait(o);
