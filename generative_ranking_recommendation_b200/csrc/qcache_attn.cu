@@ -627,10 +627,11 @@ struct Plan {
   long long units;  // blocks, or items, of one range
 };
 // From how many candidates a user the tensor-core form runs, and from how many rows for all blocks:
-// at 256 users x 480 rows of 8 heads it takes 109 us for anything up to 128 candidates, the blocks
-// 88 us for 32, 109 for 40, 129 for 48.  But its item is a long chain (31 us alone for 480 rows),
-// and blocks are faster while they find free SMs: 128 candidates x 480 rows 16 against 25 us for 1
-// user (7680 rows), 31 against 37 for 16 users (123 thousand), 53 against 31 for 32.
+// at 256 users x 480 rows of 8 heads it takes 98 us for 24 candidates, 100 for 40 and 109 for 96 and
+// 128 (8 bits: 106, 109, 111), the blocks 76 us for 24, 88 for 32, 109 for 40, 129 for 48.  But its
+// item is a long chain (31 us alone for 480 rows), and blocks are faster while they find free SMs:
+// 128 candidates x 480 rows 16 against 25 us for 1 user (7680 rows), 31 against 37 for 16 users (123
+// thousand), 53 against 31 for 32.
 constexpr int kTcFrom = 41;
 constexpr long long kTcRows = 1 << 17;
 
