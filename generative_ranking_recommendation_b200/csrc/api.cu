@@ -593,7 +593,8 @@ int genrank_qcache_read(int B, int64_t T, const int32_t* dst_offsets, const int3
 
 size_t genrank_attn_qcached_workspace_size(int B, int64_t C, int H, int dh, int max_cand,
                                            int max_len) {
-  if (B < 1 || C < 0 || H < 1 || H > kMaxHeads || dh != kQDh || max_cand < 0 || max_len < 0)
+  if (B < 1 || C < 0 || H < 1 || H > kMaxHeads || dh != kQDh || max_cand < 0 || max_len < 0 ||
+      max_len > kQMaxLen)
     return 0;
   return attn_fwd_qcached_workspace(B, C, H, max_cand, max_len);
 }
@@ -614,7 +615,7 @@ int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t* cand_offsets, int 
   if (!es || (format != GENRANK_QCACHE_INT8 && format != GENRANK_QCACHE_INT4))
     return GENRANK_ERR_INVALID_ARG;
   if (H > kMaxHeads || !use_tc(dtype, dh)) return GENRANK_ERR_UNSUPPORTED;
-  if (C >= INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
+  if (C >= INT32_MAX || max_len > kQMaxLen) return GENRANK_ERR_UNSUPPORTED;
   if (cand_stride < (int64_t)H * dh || o_stride < (int64_t)H * dh || (cand_stride * es) % 16 ||
       (o_stride * es) % 16)
     return GENRANK_ERR_INVALID_ARG;

@@ -8,6 +8,7 @@
 namespace gr {
 
 constexpr int kQDh = 64;          // values per head
+constexpr int kQMaxLen = 1 << 30;  // rows of a history
 constexpr int kQPart = kQDh + 2;  // floats of a joined range: O, then its maximum and sum
 
 // Byte offsets inside one row of H heads:

@@ -646,10 +646,10 @@ constexpr long long kTcRows = 1 << 17;
 Plan plan(int B, int H, int max_cand, int max_len) {
   Plan p;
   p.groups = (H + kHeads - 1) / kHeads;
-  p.tc = max_cand >= kTcFrom &&
-         (long long)B * p.groups * ((max_cand + kCands - 1) / kCands) * max_len >= kTcRows;
+  const long long blocks = (long long)B * p.groups * ((max_cand + kCands - 1ll) / kCands);
+  p.tc = max_cand >= kTcFrom && max_len > 0 && (blocks >= kTcRows || blocks * max_len >= kTcRows);
   const int tile = p.tc ? 128 : kCands, least = p.tc ? 256 : 64, slots = p.tc ? 296 : 148;
-  p.ctiles = max_cand > tile ? (max_cand + tile - 1) / tile : 1;
+  p.ctiles = max_cand > tile ? (int)((max_cand + tile - 1ll) / tile) : 1;
   p.units = (long long)B * (p.tc ? H : p.groups) * p.ctiles;
   auto rows = [&](long long s) { return (max_len + s * 64 - 1) / (s * 64) * 64; };
   auto cost = [&](long long s) {
@@ -659,12 +659,12 @@ Plan plan(int B, int H, int max_cand, int max_len) {
   long long best = 1;
   for (int k = 1; k <= 16; ++k) {  // whole rounds of the SMs
     long long s = (long long)slots * k / p.units;
-    const long long most = (max_len + least - 1) / least;
+    const long long most = ((long long)max_len + least - 1) / least;
     if (s > most) s = most;
     if (s > 1 && cost(s) < cost(best)) best = s;
   }
   p.chunk = (int)rows(best);
-  p.splits = p.chunk > 0 ? (max_len + p.chunk - 1) / p.chunk : 1;
+  p.splits = p.chunk > 0 ? (int)(((long long)max_len + p.chunk - 1) / p.chunk) : 1;
   return p;
 }
 
@@ -693,8 +693,8 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   int ways = 2;
   while (ways < kHalfWarps && 2 * ways < p.splits) ways *= 2;
   const int pairs = kHalfWarps / ways;  // (candidate, head) of a block
-  const long long joins = ((long long)c.a.B * c.max_cand * c.a.H + pairs - 1) / pairs;
-  if (p.units * p.splits > INT32_MAX || (p.splits > 1 && joins * pairs > INT32_MAX)) return GENRANK_ERR_UNSUPPORTED;
+  const long long joins = p.splits > 1 ? ((long long)c.a.B * c.max_cand * c.a.H + pairs - 1) / pairs : 0;
+  if (p.units * p.splits > INT32_MAX || joins * pairs > INT32_MAX) return GENRANK_ERR_UNSUPPORTED;
   Params P;
   P.c = c;
   P.groups = p.groups;
@@ -707,7 +707,7 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   const int rc = p.tc ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
                  : c.format == GENRANK_QCACHE_INT8 ? launch<GENRANK_QCACHE_INT8>(P, blocks, st)
                                                    : launch<GENRANK_QCACHE_INT4>(P, blocks, st);
-  if (rc != GENRANK_OK || p.splits == 1 || joins == 0) return rc;
+  if (rc != GENRANK_OK || joins == 0) return rc;
   // launched as soon as every block of the ranges has begun, it waits for them (grid_wait)
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

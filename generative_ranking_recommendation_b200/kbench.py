@@ -1,7 +1,7 @@
 """Per-kernel benchmark of the hot path on one workload configuration.
 
     python -m generative_ranking_recommendation_b200.kbench --config c2 \
-        [--kernels embed_fwd,attn_fwd,attn_bwd,embed_bwd,linear,bucketed,cached,hstu]
+        [--kernels embed_fwd,attn_fwd,attn_bwd,embed_bwd,linear,bucketed,cached,qcached,hstu]
         [--iters 20] [--warmup 3] [--users B]
 
 Times each library call with CUDA events around a replay of the call captured as
@@ -250,6 +250,58 @@ def main(argv=None):
                           "candidates": C, "candidates_per_s": C / ms_c * 1e3,
                           "TFLOP_per_s": 4.0 * d * cand_pairs / ms_c / 1e9,
                           "speedup_vs_full": ms_f / ms_c}), flush=True)
+
+    if "qcached" in kernels and cfg.dtype == "bf16" and dh == 64:
+        # the same candidates against the history in a quantised cache: appending every history,
+        # reading it back, and the attention over it
+        g = torch.Generator(device=dev)
+        g.manual_seed(cfg.seed)
+        qkv = torch.randn((T, 3 * d), device=dev, generator=g).to(tdt)
+        n_u = batch.hist_len.astype(np.int64)
+        cand_rows = np.concatenate([np.arange(batch.seq_offsets[u] + n_u[u], batch.seq_offsets[u + 1])
+                                    for u in range(batch.B)])
+        cr = torch.from_numpy(cand_rows).to(dev)
+        qc = qkv.index_select(0, cr).contiguous()
+        C, R = int(cr.numel()), int(n_u.sum())
+        m_u = np.diff(batch.seq_offsets).astype(np.int64) - n_u
+        coff = torch.from_numpy(np.concatenate([[0], np.cumsum(m_u)]).astype(np.int32)).to(dev)
+        first = np.concatenate([[0], np.cumsum(n_u)])
+        rows = torch.from_numpy(first[:-1].copy()).to(dev)
+        roff = torch.from_numpy(first.astype(np.int32)).to(dev)
+        ts_c = ts.index_select(0, cr).contiguous()
+        oc = torch.empty((C, d), dtype=tdt, device=dev)
+        back = torch.empty((R, 2 * d), dtype=tdt, device=dev)
+        pos_r = torch.empty(R, dtype=torch.int32, device=dev)
+        ts_r = torch.empty(R, dtype=torch.int64, device=dev)
+        m_max, n_max = int(m_u.max()), int(n_u.max())
+        ws = torch.empty(max(16, G.attn_qcached_workspace_size(batch.B, C, H, dh, m_max, n_max)),
+                         dtype=torch.uint8, device=dev)
+        for name, fmt in (("int8", G.QCACHE_INT8), ("int4", G.QCACHE_INT4)):
+            row = G.qcache_row_bytes(H, dh, fmt)
+            cache = torch.zeros((R, row), dtype=torch.uint8, device=dev)
+
+            def fa():
+                G.qcache_append(off, hl, qkv[:, d:], qkv[:, 2 * d:], 3 * d, H, dh, pos, ts, cache,
+                                rows, fmt, err, T=T)
+
+            def fr():
+                G.qcache_read(roff, None, cache, rows, back, back[:, d:], 2 * d, H, dh, pos_r, ts_r,
+                              fmt, err, T=R)
+
+            def fs():
+                G.attn_fwd_qcached(coff, m_max, qc, qc[:, d:], qc[:, 2 * d:], 3 * d, cache, rows,
+                                   hl, n_max, ts_c, H, dh, sp, st, scale, oc, d, None, ws, fmt,
+                                   err, C=C)
+
+            ms_a = timed(fa, args.iters, args.warmup, flush)
+            ms_r = timed(fr, args.iters, args.warmup, flush)
+            ms_s = timed(fs, args.iters, args.warmup, flush)
+            print(json.dumps({**base, "kernel": f"qcached_{name}", "append_ms": ms_a,
+                              "append_GB_per_s": R * (row + 4 * d) / ms_a / 1e6, "read_ms": ms_r,
+                              "read_GB_per_s": R * (row + 4 * d) / ms_r / 1e6, "ms": ms_s,
+                              "candidates": C, "candidates_per_s": C / ms_s * 1e3,
+                              "TFLOP_per_s": 4.0 * d * int(np.sum(m_u * n_u + m_u)) / ms_s / 1e9}),
+                  flush=True)
 
     if "hstu" in kernels:
         # the interleaved layout (2n + m tokens) with a dense N x N bias read from HBM,

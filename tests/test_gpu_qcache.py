@@ -502,6 +502,14 @@ def test_more_items_than_blocks(G):
         _check(G, *_batch(43, users, 4, bits), max_cand=128, max_len=1000)
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+def test_small_caches_and_loose_bounds(G, bits):
+    """Caches and candidate arrays shorter than a tile, and bounds far beyond what is there."""
+    for users in ([(1, 50)], [(0, 41), (3, 2)], [(40, 3)]):
+        for kw in (WIDE, dict(max_len=1 << 30), dict(max_cand=5000, max_len=100000)):
+            _check(G, *_batch(53, users, 2, bits, slack=0), **kw)
+
+
 def test_short_items_in_a_row(G):
     """Blocks walk over a dozen items each of no tile, one or two, and few or many candidates, whose
     roles' warps take different time."""

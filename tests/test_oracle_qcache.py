@@ -167,6 +167,7 @@ def test_attention_refusals(L):
     assert call(dtype=0) == 2  # fp32 candidates
     assert call(dh=128, stride=1536, ostride=512) == 2
     assert call(H=65, stride=3 * 65 * 64, ostride=65 * 64) == 2
+    assert call(max_len=(1 << 30) + 1) == 2
     assert call(ws=None) == 3
     assert call(wsb=16) == 3
     assert call(ws=P(0x10004)) == 3
@@ -181,6 +182,10 @@ def test_workspace_and_row_sizes(L):
     assert ws(1, 1, 8, 64, 1, 4096) > 0      # few blocks: ranges of the history are joined
     assert ws(4096, 4096, 8, 64, 1, 480) == 0
     assert ws(1, 1, 8, 64, 1, 0) == 0
+    # the largest bounds
+    assert ws(1, 1, 8, 64, 1, 1 << 30) > 0 and ws(1, 1, 8, 64, 1, (1 << 30) + 1) == 0
+    assert ws(2**31 - 1, 1, 64, 64, 2**31 - 1, 1 << 30) == 0
+    assert ws(1, 1, 8, 64, 2**31 - 1, 1 << 30) == 0
     for args in ((0, 1, 8, 64, 1, 10), (1, -1, 8, 64, 1, 10), (1, 1, 8, 32, 1, 10), (1, 1, 65, 64, 1, 10),
                  (1, 1, 8, 64, -1, 10), (1, 1, 8, 64, 1, -1)):
         assert ws(*args) == 0
