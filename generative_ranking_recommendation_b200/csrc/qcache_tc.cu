@@ -284,26 +284,32 @@ GR_DEVICE uint4* chunk_at(uint8_t* tile, int row, int c) {
   return reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
+// Shared-memory address of that row's chunk 0; chunk c is at it ^ 16 c (tiles start at multiples of
+// 128 bytes).
+GR_DEVICE uint32_t row_addr(const uint8_t* tile, int row) { return smem_u32(tile) + row * 128 + ((row & 7) << 4); }
+GR_DEVICE void store16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // A row's 64 values, code times f, as fp16 in the tile.  4 bits: the eight values
 // of a word go out as 0 4 1 5 2 6 3 7, the order in which masks take them out (Q has the same
 // order, and O's columns are put back when they are written).
 template <int FMT>
-GR_DEVICE void store_codes(const uint8_t* from, float f, uint8_t* tile, int row) {
+GR_DEVICE void store_codes(const uint8_t* from, float f, uint32_t to) {  // to: row_addr
   const uint32_t f2 = pack_f16(f, f);
   if constexpr (FMT == GENRANK_QCACHE_INT4) {
     // high nibbles: (1024 + 16 u) f / 16 - 72 f = (u - 8) f, every factor exact
     const uint32_t f16th = mul_f16(f2, 0x2C002C00u), m72 = mul_f16(f2, 0xD480D480u);
-#pragma unroll 1
+#pragma unroll
     for (int c = 0; c < 8; c += 4) {
       const uint4 x = *reinterpret_cast<const uint4*>(from + 4 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w, v = w >> 8;
-        *chunk_at(tile, row, c + i) =
-            make_uint4(mul_f16(sub_f16((w & 0x000F000Fu) | 0x64006400u, 0x64086408u), f2),
-                       fma_f16((w & 0x00F000F0u) | 0x64006400u, f16th, m72),
-                       mul_f16(sub_f16((v & 0x000F000Fu) | 0x64006400u, 0x64086408u), f2),
-                       fma_f16((v & 0x00F000F0u) | 0x64006400u, f16th, m72));
+        store16(to ^ (16 * (c + i)), mul_f16(sub_f16((w & 0x000F000Fu) | 0x64006400u, 0x64086408u), f2),
+                fma_f16((w & 0x00F000F0u) | 0x64006400u, f16th, m72),
+                mul_f16(sub_f16((v & 0x000F000Fu) | 0x64006400u, 0x64086408u), f2),
+                fma_f16((v & 0x00F000F0u) | 0x64006400u, f16th, m72));
       }
     }
   } else {
@@ -314,11 +320,10 @@ GR_DEVICE void store_codes(const uint8_t* from, float f, uint8_t* tile, int row)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t w = i ? x.z : x.x, v = i ? x.w : x.y;
-        *chunk_at(tile, row, c + i) =
-            make_uint4(fma_f16(__byte_perm(w, 0x64646464u, 0x4140), f2, m1152),
-                       fma_f16(__byte_perm(w, 0x64646464u, 0x4342), f2, m1152),
-                       fma_f16(__byte_perm(v, 0x64646464u, 0x4140), f2, m1152),
-                       fma_f16(__byte_perm(v, 0x64646464u, 0x4342), f2, m1152));
+        store16(to ^ (16 * (c + i)), fma_f16(__byte_perm(w, 0x64646464u, 0x4140), f2, m1152),
+                fma_f16(__byte_perm(w, 0x64646464u, 0x4342), f2, m1152),
+                fma_f16(__byte_perm(v, 0x64646464u, 0x4140), f2, m1152),
+                fma_f16(__byte_perm(v, 0x64646464u, 0x4342), f2, m1152));
       }
     }
   }
@@ -464,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
     // ---------------------------------------------------------------- operands
     const int d = threadIdx.x - 128;
     const int side = d >> 6, key = d & 63;  // K or V row of a tile
+    const uint32_t tile0 = row_addr(smem + (side == 0 ? kOffK : kOffV), key);
     int qi = 0, g = 0;
     bool ok = true;
     while (ok) {
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           break;
         }
         if (side == 0) reinterpret_cast<uint4*>(smem + kOffKA + st * kKABytes)[key] = term4;
-        store_codes<FMT>(from + (side * BN + key) * R::kCb, f, smem + (side == 0 ? kOffK : kOffV) + st * kTileBytes, key);
+        store_codes<FMT>(from + (side * BN + key) * R::kCb, f, tile0 + st * kTileBytes);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -726,6 +732,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       uint4 k_next[2] = {load_k(0), load_k(1)};
       if (!wait_warp(&bars[kQRaw + qb], par(qi >> 1), abort_flag)) return false;
       const int rows4 = (nx.mt - 32 * w4 + 3) >> 2;  // rows of candidates, by fours
+      float own_dot = 0.f;  // of the lane's own row, and its exponent
+      int own_qe = 0;
 #pragma unroll 1
       for (int i = 0; i < min(rows4, 8); ++i) {
         const uint4 k4 = k_next[0];
@@ -756,7 +764,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         // 2^-43 of a score)
         int qe = min(max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -126), 126);
         qe = max(qe, min(kMinUp - nx.ke, 126));
-        const int up = min(qe + nx.ke, 126);
         const float qd = pow2(-qe);
         float f[8];
 #pragma unroll
@@ -764,15 +771,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         *place = FMT == GENRANK_QCACHE_INT4
                      ? make_uint4(pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7]))
                      : make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
-        const float t_row = __shfl_sync(0xffffffffu, term, at);
-        if (ch == 0) {
-          const uint32_t one = __float_as_uint(pow2(max(-up, -126))) >> 16;
-          reinterpret_cast<uint4*>(smem + kOffQA + qb * kQABytes)[row] = make_uint4(one | (one << 16), one, 0u, 0u);
-          float* rd = rowdata + qb * 4 * BM + row;
-          rd[0] = sl2 * pow2(max(up, -126));
-          rd[BM] = fmaf(dot, sl2, t_row);
-          rd[2 * BM] = t_row;
+        // the row's lane is 4 i + sub
+        const float d = __shfl_sync(0xffffffffu, dot, 8 * (lane & 3));
+        const int e = __shfl_sync(0xffffffffu, qe, 8 * (lane & 3));
+        if (i == lane >> 2) {
+          own_dot = d;
+          own_qe = e;
         }
+      }
+      if (32 * w4 < nx.mt) {
+        const int up = min(own_qe + nx.ke, 126);
+        const uint32_t one = __float_as_uint(pow2(max(-up, -126))) >> 16;
+        reinterpret_cast<uint4*>(smem + kOffQA + qb * kQABytes)[r] = make_uint4(one | (one << 16), one, 0u, 0u);
+        float* rd = rowdata + qb * 4 * BM + r;
+        rd[0] = sl2 * pow2(max(up, -126));
+        rd[BM] = fmaf(own_dot, sl2, term);
+        rd[2 * BM] = term;
       }
       fence_proxy_async_smem();
       __syncwarp();
