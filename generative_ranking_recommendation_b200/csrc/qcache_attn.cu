@@ -43,7 +43,7 @@ namespace qca {
 constexpr int kHeads = 8;    // heads of a block, one warp each
 constexpr int kCands = 8;    // candidates of a block
 constexpr int kStages = 3;   // tiles in flight
-constexpr int kThreads = (kHeads + 1) * 32;
+constexpr int kMaxThreads = (kHeads + 1) * 32;  // the heads' warps and the one that copies
 constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
 constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
 constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
@@ -212,7 +212,7 @@ GR_DEVICE float group_sum(float x) {
 
 // A tile is 32 SUB rows, whose chains of loads, products and exponentials overlap.
 template <int FMT, int SUB>
-__global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kMaxThreads) k_qcached(const __grid_constant__ Params P) {
   constexpr int kRows = 32 * SUB;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kStages], ready[kStages], empty[kStages];
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) k_qcached(const __grid_constant__ Pa
   __syncthreads();
 
   const long long t_ref = a.ts[c0];
-  if (warp == kHeads) {
+  if (warp == (int)blockDim.x / 32 - 1) {
     // ------------------------------------------------------------------ copies and distances
     const uint8_t* src = c.cache + (at + lo) * (long long)L.bytes;
     const int scale_bytes = (4 * heads + 15) / 16 * 16;
@@ -674,9 +674,10 @@ template <int FMT>
 int launch(const Params& P, unsigned blocks, cudaStream_t st) {
   static DeviceOnce once;
   constexpr int sub = FMT == GENRANK_QCACHE_INT4 ? 2 : 1, rows = kStages * 32 * sub;
+  const int heads = P.c.a.H < kHeads ? P.c.a.H : kHeads;
   if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, sub>, rows * qrow(kHeads, FMT).bytes))
     return GENRANK_ERR_CUDA;
-  k_qcached<FMT, sub><<<blocks, kThreads, rows * qrow(P.c.a.H < kHeads ? P.c.a.H : kHeads, FMT).bytes, st>>>(P);
+  k_qcached<FMT, sub><<<blocks, (heads + 1) * 32, rows * qrow(heads, FMT).bytes, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
 }
 
