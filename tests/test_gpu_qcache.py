@@ -362,6 +362,18 @@ def test_many_users(G):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+def test_many_users_of_unequal_length(G, bits):
+    """More blocks than fit at once, the longer histories first: lengths on both sides of half the
+    bound, and exactly half."""
+    r = np.random.default_rng(10)
+    users = [(int(r.choice([0, 1, 299, 300, 301, 600])), int(r.integers(0, 3))) for _ in range(500)]
+    batch, values = _batch(10, users, 2, bits)
+    _check(G, batch, values, max_len=600)
+    _, _, code = _score(G, **dict(batch, cache=_dev(batch["cache"])), max_len=599)
+    assert code == G.DERR["LAYOUT"]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 def test_unequal_magnitudes(G, bits):
     """V scales over 2^+-20 within a history, and scores of some hundreds: the running maximum
     and the range of P move often; a candidate's own score far above and far below the rest."""
