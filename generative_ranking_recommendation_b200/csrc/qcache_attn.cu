@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_qcached(const __grid_constant__
   volatile int* abort_flag = &abort_word;
   const QcachedAttnArgs& c = P.c;
   const AttnArgs& a = c.a;
-  grid_release();
+  if (P.part) grid_release();  // the join may be set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Work w = work_of(P, blockIdx.x);
   int c0, m, n;

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const QcachedAttnArgs& c = P.c;
   const AttnArgs& a = c.a;
-  grid_release();
+  if (P.part) grid_release();  // the join may be set up
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);

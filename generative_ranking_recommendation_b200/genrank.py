@@ -370,7 +370,7 @@ def _device_of(what, t):
     dev = t.get_device()
     if dev < 0:
         raise GenRankError(f"{what}: tensors on {t.device}: the library runs on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise GenRankError(f"{what}: tensors on cuda:{dev}, but the current device is "
                            f"cuda:{torch.cuda.current_device()}")
     return dev
@@ -394,12 +394,14 @@ def _mat(what, name, t, dev, dtype, rows, stride, width):
     lie inside its storage."""
     if t.dtype is not dtype or t.get_device() != dev:
         raise GenRankError(f"{what}: {name} must be {dtype} on cuda:{dev} (got {t.dtype} on {t.device})")
-    if rows > 0 and not (t.dim() == 2 and t.shape[0] >= rows and t.stride(0) == stride
-                         and t.shape[1] >= width and t.stride(1) == 1):
-        end = (t.storage_offset() + (rows - 1) * stride + width) * t.element_size()
-        if end > t.untyped_storage().nbytes():
-            raise GenRankError(f"{what}: {name} has fewer than {rows} rows of {width} values, "
-                               f"{stride} apart")
+    if rows > 0:
+        shape, strides = t.shape, t.stride()
+        if not (len(shape) == 2 and shape[0] >= rows and strides[0] == stride
+                and shape[1] >= width and strides[1] == 1):
+            end = (t.storage_offset() + (rows - 1) * stride + width) * t.element_size()
+            if end > t.untyped_storage().nbytes():
+                raise GenRankError(f"{what}: {name} has fewer than {rows} rows of {width} values, "
+                                   f"{stride} apart")
     return t.data_ptr()
 
 
