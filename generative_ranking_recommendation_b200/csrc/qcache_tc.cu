@@ -318,7 +318,7 @@ GR_DEVICE void store_codes(const uint8_t* from, float f, uint32_t to) {  // to: 
     }
   } else {
     const uint32_t m1152 = mul_f16(f2, 0xE480E480u);  // exact: the scale is a power of two
-#pragma unroll 2
+#pragma unroll
     for (int c = 0; c < 8; c += 2) {
       const uint4 x = *reinterpret_cast<const uint4*>(from + 8 * c);
 #pragma unroll
