@@ -216,7 +216,7 @@ GR_DEVICE float group_sum(float x) {
 
 // A tile is 32 SUB rows, whose chains of loads, products and exponentials overlap.
 template <int FMT, int SUB>
-__global__ void __launch_bounds__(kMaxThreads) k_qcached(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const __grid_constant__ Params P) {
   constexpr int kRows = 32 * SUB;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kStages], ready[kStages], empty[kStages];
@@ -673,16 +673,19 @@ Plan plan(int B, int H, int max_cand, int max_len) {
   return p;
 }
 
-// Tiles of 64 rows of 4 bits (156 us against 165 us with 32, at 256 users x 4096 rows) or 32 of 8
-// bits: about 100 KB of stages for each of two blocks an SM.
-template <int FMT>
+// Tiles of 64 rows of 4 bits (150 us against 165 us with 32, at 256 users x 4096 rows) or 32 of 8
+// bits: about 100 KB of stages for each of two blocks an SM.  Short histories take no more stages
+// than they fill, and tiles of 32 rows, whose registers allow a third block (1000 users of 10 rows,
+// 41 candidates: 143 -> 96 us).
+template <int FMT, int SUB>
 int launch(const Params& P, unsigned blocks, cudaStream_t st) {
   static DeviceOnce once;
-  constexpr int sub = FMT == GENRANK_QCACHE_INT4 ? 2 : 1, rows = kStages * 32 * sub;
+  constexpr int tile = 32 * SUB;
   const int heads = P.c.a.H < kHeads ? P.c.a.H : kHeads;
-  if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, sub>, rows * qrow(kHeads, FMT).bytes))
+  const int stages = P.chunk >= kStages * tile ? kStages : (P.chunk + tile - 1) / tile;
+  if (!set_smem_limit_once(once, (const void*)k_qcached<FMT, SUB>, kStages * tile * qrow(kHeads, FMT).bytes))
     return GENRANK_ERR_CUDA;
-  k_qcached<FMT, sub><<<blocks, (heads + 1) * 32, rows * qrow(heads, FMT).bytes, st>>>(P);
+  k_qcached<FMT, SUB><<<blocks, (heads + 1) * 32, stages * tile * qrow(heads, FMT).bytes, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? GENRANK_OK : GENRANK_ERR_LAUNCH;
 }
 
@@ -717,8 +720,9 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   const bool twice = !p.tc && p.splits == 1 && p.units > 444 && p.units < c.max_len;
   const unsigned blocks = twice ? 2 * P.first : P.first;
   const int rc = p.tc ? launch_qcached_tc(c, p.ctiles, p.splits, p.chunk, P.part, st)
-                 : c.format == GENRANK_QCACHE_INT8 ? launch<GENRANK_QCACHE_INT8>(P, blocks, st)
-                                                   : launch<GENRANK_QCACHE_INT4>(P, blocks, st);
+                 : c.format == GENRANK_QCACHE_INT8 ? launch<GENRANK_QCACHE_INT8, 1>(P, blocks, st)
+                 : c.max_len <= kStages * 32 ? launch<GENRANK_QCACHE_INT4, 1>(P, blocks, st)
+                                   : launch<GENRANK_QCACHE_INT4, 2>(P, blocks, st);
   if (rc != GENRANK_OK || joins == 0) return rc;
   // launched as soon as every block of the ranges has begun, it waits for them (grid_wait)
   cudaLaunchAttribute early;
