@@ -27,9 +27,9 @@
 //     candidate's own score: most tiles take one vote and no shuffles.
 //   * Short of blocks, the history is cut into ranges; the ranges' (max, sum, O) in fp32 are
 //     joined by a second kernel, always in the same order.
-// Bound: with one candidate the copies, at 256 users x 4096 rows of 8 heads 156 us for int4 rows
-// (587 MB, 3.8 TB/s; the copies alone take 117) and 199 us for int8 (1124 MB, 5.7 TB/s); with more
-// the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 88 us).
+// Bound: with one candidate the copies, at 256 users x 4096 rows of 8 heads 150 us for int4 rows
+// (587 MB, 3.9 TB/s; the copies alone take 117) and 200 us for int8 (1124 MB, 5.6 TB/s); with more
+// the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 84 us).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -633,7 +633,7 @@ struct Plan {
 };
 // From how many candidates a user the tensor-core form runs, and from how many rows for all blocks:
 // at 256 users x 480 rows of 8 heads it takes 98 us for 24 candidates, 100 for 40 and 109 for 96 and
-// 128 (8 bits: 106, 109, 111), the blocks 76 us for 24, 88 for 32, 109 for 40, 129 for 48.  But its
+// 128 (8 bits: 106, 109, 111), the blocks 76 us for 24, 84 for 32, 109 for 40, 129 for 48.  But its
 // item is a long chain (31 us alone for 480 rows), and blocks are faster while they find free SMs:
 // 128 candidates x 480 rows 16 against 25 us for 1 user (7680 rows), 31 against 37 for 16 users (123
 // thousand), 53 against 31 for 32.
