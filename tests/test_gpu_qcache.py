@@ -345,6 +345,15 @@ def test_attention(G, bits, users, H):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("most", [0, 1, 32, 33, 64, 65, 96, 97])
+def test_short_histories(G, bits, most):
+    """Blocks that stage no more tiles than the bound needs, up to all of them."""
+    lens = [n for n in (0, 1, 31, 32, 33, 63, 64, 65, 95, 96, 97) if n <= most]
+    users = [(n, 1 + (3 * i) % 11) for i, n in enumerate(lens * 8)]
+    _check(G, *_batch(most, users, 9, bits), extra=1)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("n,m,H", [(1, 1, 8), (480, 1, 8), (1000, 8, 3), (4097, 1, 8), (2051, 33, 2), (9000, 2, 17),
                                    (64, 1, 64), (65, 300, 1)])
 def test_one_user_in_ranges(G, bits, n, m, H):
