@@ -392,7 +392,8 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  * candidate) counts as zero.
  * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, a head scaled
  * by a power of two: exact down to 2^-17 of its largest element, 2^-25 of that below; softmax
- * weights are rounded to fp16's 11 bits. */
+ * weights are rounded to fp16's 11 bits.  With many candidates, rows whose scale is below 2^-25
+ * (int4; 2^-30 int8) of the largest of the head's history lose low bits. */
 int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t *cand_offsets, int max_cand,
                              const void *q_c, const void *k_c, const void *v_c,
                              int64_t cand_stride, const void *cache, int64_t R,
