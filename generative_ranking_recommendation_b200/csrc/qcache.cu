@@ -45,11 +45,12 @@ struct Walk {
   int first = 0, last = 0, end = 0;  // the user's rows [first, last) are copied, [first, end) are its
   long long at = 0;                  // cache row of token row 0 (first's less first)
 
-  // The first such row at or after t, or t1.
+  // The first such row at or after t, or one at or behind t1.  Rows before the first user's segment
+  // are nobody's; where offsets do not ascend (flagged), a row is the first user's found to hold it.
   GR_DEVICE int next(const QcacheArgs& a, int t, int t1) {
     while (t < t1) {
       if (u < 0 || t >= end) {
-        u = u < 0 || t > end ? warp_find_user(a.off, a.B, t) : u + 1;
+        u = u < 0 ? warp_find_user(a.off, a.B, t) : u + 1;
         if (u >= a.B) return t1;  // rows behind the last user
         first = a.off[u];
         end = a.off[u + 1];
@@ -57,9 +58,9 @@ struct Walk {
         last = user_rows<kWrite>(a, u, first, end, n, at) ? first + n : first;
         at -= first;
       }
-      if (t < first || t > end) return t1;  // offsets that do not ascend: flagged
+      t = max(t, first);
       if (t < last) return t;
-      t = end;
+      t = max(t, end);
     }
     return t1;
   }

@@ -350,13 +350,16 @@ size_t genrank_qcache_row_bytes(int H, int dh, int format);
  * seq_offsets, src_len = hist_len, k and v views of the fused projection) and one new token
  * of each user (src_offsets = 0..B, src_len = NULL, rows = first row + tokens held) are the
  * same call.
- *   src_offsets [B+1] int32 into the T token rows; src_len [B] int32, or NULL for all of a
- *                user's segment; k, v: [T] rows of H * 64 values in dtype (GENRANK_F32 or
- *                GENRANK_BF16), row stride tok_stride elements, 16-byte aligned rows
+ *   src_offsets [B+1] int32 into the T token rows, ascending from any first row (rows before
+ *                src_offsets[0] and from src_offsets[B] on are nobody's); src_len [B] int32, or
+ *                NULL for all of a user's segment; k, v: [T] rows of H * 64 values in dtype
+ *                (GENRANK_F32 or GENRANK_BF16), row stride tok_stride elements, 16-byte aligned
+ *                rows
  *   pos [T] int32 (1-based), ts [T] int64 seconds
  *   rows [B] int64: ascending, user u's range ending at or before rows[u+1] (users without
  *                new rows included), so that no two users write one row
- * A user whose ranges break these rules sets GENRANK_DERR_LAYOUT and is left out. */
+ * A user whose ranges break these rules sets GENRANK_DERR_LAYOUT and is left out; where offsets
+ * do not ascend, so may be users behind that place. */
 int genrank_qcache_append(int B, int64_t T, const int32_t *src_offsets, const int32_t *src_len,
                           const void *k, const void *v, int64_t tok_stride, int H, int dh,
                           int dtype, const int32_t *pos, const int64_t *ts, int format,

@@ -854,3 +854,66 @@ def test_python_refusals_on_the_gpu(G):
         with pytest.raises(G.GenRankError):
             append(**kw)
     assert G.check_error(err) == 0
+
+
+# ------------------------------------------------------------------------------------------
+# long token arrays: a warp walks several rows
+# ------------------------------------------------------------------------------------------
+
+def _long_batch(seed, T, first, H, bits):
+    """Segments of every length from offset `first` on, some rows of each written, rows of nobody
+    behind the last; tokens out of a pool of 300 and the pool's cache rows."""
+    r = np.random.default_rng(seed)
+    seg = []
+    while first + sum(seg) < T - 2100:
+        seg.append(int(r.choice([0, 0, 1, 2, 7, 64, 300, 2000])))
+    seg = np.array(seg)
+    length = np.array([int(r.integers(0, s + 1)) if r.random() < 0.5 else s for s in seg])
+    off = first + np.concatenate([[0], np.cumsum(seg)])
+    k, v = _kv(r, 300, H, 6.0), _kv(r, 300, H, 6.0)
+    pos, ts = r.integers(1, 1000, 300), r.integers(0, 1 << 40, 300)
+    at = np.concatenate([[0], np.cumsum(length + r.integers(0, 3, len(seg)))]) + 1
+    of = np.concatenate([np.arange(o, o + n) for o, n in zip(off, length)])  # token rows copied
+    to = np.concatenate([np.arange(a, a + n) for a, n in zip(at, length)])   # and their cache rows
+    return dict(off=off, length=length, k=k, v=v, pos=pos, ts=ts, at=at, of=of, to=to, token=r.integers(0, 300, T),
+                pool=oracle.qcache_rows(k, v, pos, ts, bits))
+
+
+LONG = [(1, 200000, 5), (8, 40000, 1), (9, 30000, 481), (2, 20000, 0)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("H,T,first", LONG)
+def test_append_long_arrays(G, bits, H, T, first):
+    b = _long_batch(T + first, T, first, H, bits)
+    i = b["token"]
+    R = int(b["at"][-1]) + 2
+    cache, code = _append(G, b["k"][i], b["v"][i], b["pos"][i], b["ts"][i], b["off"], b["length"], b["at"][:-1], R, bits)
+    assert code == 0
+    want = np.full((R, cache.shape[1]), 0x5A, np.uint8)
+    want[b["to"]] = b["pool"][i[b["of"]]]
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("H,T,first", LONG)
+def test_read_long_arrays(G, bits, H, T, first):
+    b = _long_batch(T + first, T, first, H, bits)
+    r = np.random.default_rng(first)
+    at = r.integers(0, 5000 - 2000, len(b["length"]))  # rows in any order, shared by users
+    token = r.integers(0, 300, 5000)
+    out = torch.full((2, T, H * 64), -7.0, dtype=torch.bfloat16, device="cuda")
+    po = torch.full((T,), -7, dtype=torch.int32, device="cuda")
+    to = torch.full((T,), -7, dtype=torch.int64, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.qcache_read(_dev(b["off"], torch.int32), _dev(b["length"], torch.int32), _dev(b["pool"][token]), _dev(at, torch.int64),
+                  out[0], out[1], H * 64, H, 64, po, to, _fmt(G, bits), err)
+    assert G.check_error(err) == 0
+    src = token[np.concatenate([np.arange(a, a + n) for a, n in zip(at, b["length"])])]
+    for side, x in enumerate((b["k"], b["v"])):
+        want = np.full((T, H * 64), -7.0, np.float32)
+        want[b["of"]] = oracle.qcache_values(x, bits).reshape(300, -1)[src]
+        assert np.array_equal(out[side].float().cpu().numpy(), want)
+    wp, wt = np.full(T, -7), np.full(T, -7)
+    wp[b["of"]], wt[b["of"]] = b["pos"][src], b["ts"][src]
+    assert np.array_equal(po.cpu().numpy(), wp) and np.array_equal(to.cpu().numpy(), wt)
