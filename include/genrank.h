@@ -358,8 +358,9 @@ size_t genrank_qcache_row_bytes(int H, int dh, int format);
  *   pos [T] int32 (1-based), ts [T] int64 seconds
  *   rows [B] int64: ascending, user u's range ending at or before rows[u+1] (users without
  *                new rows included), so that no two users write one row
- * A user whose ranges break these rules sets GENRANK_DERR_LAYOUT and is left out; where offsets
- * do not ascend, so may be users behind that place. */
+ * A user whose ranges break these rules sets GENRANK_DERR_LAYOUT and is left out.  Where offsets
+ * do not ascend, users behind that place may be left out as well, and where first rows do not,
+ * users whose range is not in order with every other user's. */
 int genrank_qcache_append(int B, int64_t T, const int32_t *src_offsets, const int32_t *src_len,
                           const void *k, const void *v, int64_t tok_stride, int H, int dh,
                           int dtype, const int32_t *pos, const int64_t *ts, int format,

@@ -917,3 +917,42 @@ def test_read_long_arrays(G, bits, H, T, first):
     wp, wt = np.full(T, -7), np.full(T, -7)
     wp[b["of"]], wt[b["of"]] = b["pos"][src], b["ts"][src]
     assert np.array_equal(po.cpu().numpy(), wp) and np.array_equal(to.cpu().numpy(), wt)
+
+
+def test_append_never_writes_a_row_twice(G):
+    """Users whose first rows do not ascend: whatever is left out, those written are whole and apart
+    from one another, a user in order with all others is written, and the call is flagged."""
+    r = np.random.default_rng(70)
+    n_tok, H, bits = 400, 1, 4
+    k, v = _kv(r, n_tok, H), _kv(r, n_tok, H)
+    pos, ts = np.arange(n_tok), np.arange(n_tok)
+    rows_of = oracle.qcache_rows(k, v, pos, ts, bits)
+    shapes = [([0, 50, 3], [5, 1, 5]), ([0, 50, 3, 4], [5, 1, 1, 1]), ([3, 50, 0, 1, 2], [5, 1, 1, 1, 9]),
+              ([90, 5, 5, 5, 7], [1, 2, 2, 0, 0])]
+    for _ in range(60):
+        B = int(r.integers(2, 40))
+        n = r.integers(0, 9, B)
+        at = np.concatenate([[0], np.cumsum(n)])[:-1] + 3
+        for _ in range(int(r.integers(0, 4))):  # some moved, or swapped
+            i, j = r.integers(0, B, 2)
+            at[i] = at[j] if r.random() < 0.5 else int(r.integers(-2, 420))
+        shapes.append((at, n))
+    for at, n in shapes:
+        at, n = np.asarray(at, np.int64), np.asarray(n)
+        off = np.concatenate([[0], np.cumsum(n)])
+        T, R = int(off[-1]) + 1, 410
+        cache, code = _append(G, k[:T], v[:T], pos[:T], ts[:T], off, None, at, R, bits)
+        got = cache.cpu().numpy()
+        end = at + n
+        fits = (at >= 0) & (end <= R)
+        good = bool(fits.all() and (end[:-1] <= at[1:]).all())
+        assert (code == 0) == good and code in (0, G.DERR["LAYOUT"])
+        written = np.zeros(R, int)
+        for u in range(len(n)):
+            in_order = fits[u] and (end[:u] <= at[u]).all() and (at[u + 1:] >= end[u]).all() and (at[:u] <= at[u]).all()
+            whole = bool(fits[u]) and np.array_equal(got[at[u]:end[u]], rows_of[off[u]:off[u + 1]])
+            assert whole or not in_order
+            if whole:
+                written[at[u]:end[u]] += 1
+        assert written.max(initial=0) <= 1
+        assert np.array_equal(written > 0, (got != 0x5A).any(-1))
