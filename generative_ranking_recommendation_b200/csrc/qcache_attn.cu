@@ -335,11 +335,11 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
   const float sp2 = a.slope_pos[h] * kLog2e, st2 = a.slope_time[h] * kLog2e;
   const float sc2 = a.scale * kLog2e;
 
-  // q as the B operand (candidate g), scaled by a power of two into fp16's range, and each
-  // candidate's own score
+  // q as the B operand (candidate g), each scaled by its own power of two into fp16's range, and
+  // each candidate's own score
   uint32_t q[4][2];
   float self[2];  // of candidates 2t, 2t + 1: the lane's accumulator columns
-  float qs;
+  uint64_t qs2;   // their scales, q's power of two included
   {
     const long long ci = cb + min(g, mt - 1);
     const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + ci * a.tok_stride + h * kQDh;
@@ -359,11 +359,12 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
     }
     dot += __shfl_xor_sync(0xffffffffu, dot, 1);
     dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
     const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-    qs = __uint_as_float((uint32_t)(127 + ex) << 23) * sc2;
+    const float qs = __uint_as_float((uint32_t)(127 + ex) << 23) * sc2;
+    qs2 = f2_pack(__shfl_sync(0xffffffffu, qs, 8 * t), __shfl_sync(0xffffffffu, qs, 8 * t + 4));
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
       const int row = 32 * z + lane;
       const uint32_t sc = *reinterpret_cast<const uint32_t*>(base + sc_at + row * S.bytes);
       const float4 gp = gaps[st][row];
-      key_scale[z] = bf16_lo(sc) * qs;
+      key_scale[z] = bf16_lo(sc);
       key_bias[z] = fmaf(sp2, gp.x, fmaf(st2, gp.y, gp.z));
       value_scale[z] = bf16_hi(sc);
       v_max = fmaxf(v_max, value_scale[z]);
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
         const int of = 16 * (kk & 1) + kr0 + e;
         const float ksc = __shfl_sync(0xffffffffu, key_scale[kk / 2], of);
         const float col = __shfl_sync(0xffffffffu, key_bias[kk / 2], of);
-        f2_unpack(f2_fma(f2_pack(acc[2 * e], acc[2 * e + 1]), f2_pack(ksc, ksc), f2_pack(col, col)), s[kk][2 * e],
+        f2_unpack(f2_fma(f2_pack(acc[2 * e], acc[2 * e + 1]), f2_mul(f2_pack(ksc, ksc), qs2), f2_pack(col, col)), s[kk][2 * e],
                   s[kk][2 * e + 1]);
       }
     }
@@ -465,7 +466,9 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
       float al[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float next = fmaxf(mx[e], group_max(best[e]));
+        // (a candidate's maximum is its own affair: it does not move because a neighbour's does)
+        const float top_e = group_max(best[e]);
+        const float next = top_e > mx[e] + kSlack ? top_e : mx[e];
         al[e] = ex2(mx[e] - next);
         mx[e] = next;
 #pragma unroll

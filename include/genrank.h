@@ -394,9 +394,10 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  * (a cached time after a candidate's), GENRANK_DERR_POS_RANGE (a cached position outside
  * [0, n_u + 1]); in the last two cases a distance below zero (in time: from the user's first
  * candidate) counts as zero.
- * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, a head scaled
- * by a power of two: exact down to 2^-17 of its largest element, 2^-25 of that below; softmax
- * weights are rounded to fp16's 11 bits.  With many candidates, rows whose scale is below 2^-25
+ * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, each head of
+ * each candidate scaled by a power of two of its own: exact down to 2^-17 of its largest element,
+ * 2^-25 of that below; softmax weights are rounded to fp16's 11 bits.  Under the same bounds a
+ * candidate's result is the same bits whatever other candidates there are.  With many candidates, rows whose scale is below 2^-25
  * (int4; 2^-30 int8) of the largest of the head's history lose low bits. */
 int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t *cand_offsets, int max_cand,
                              const void *q_c, const void *k_c, const void *v_c,

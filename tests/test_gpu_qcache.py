@@ -956,3 +956,22 @@ def test_append_never_writes_a_row_twice(G):
                 written[at[u]:end[u]] += 1
         assert written.max(initial=0) <= 1
         assert np.array_equal(written > 0, (got != 0x5A).any(-1))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("m,kw", [(8, {}), (8, WIDE), (40, WIDE)], ids=["few", "many", "40"])
+def test_a_candidate_beside_an_outlier(G, bits, m, kw):
+    """One candidate's q a factor up to 2^60 above the others': each keeps its own precision, and
+    is bit for bit what it is alone (under the same bounds)."""
+    batch, values = _batch(60, [(480, m)], 3, bits)
+    few = not kw
+    kw = dict(kw or dict(max_cand=m, max_len=480))
+    plain = batch["qkv"]
+    for up in (12, 17, 20, 24, 60) if few else (12, 17, 20, 24):
+        batch["qkv"] = plain.copy()
+        batch["qkv"][0, 1] *= np.float32(2.0 ** up)
+        o, lse, _ = _check(G, batch, values, **kw)
+        for c in (0, 1, 5, m - 1):
+            one, ls, code = _score(G, batch["qkv"][:, c:c + 1], [0, 1], _dev(batch["cache"]), batch["rows"], batch["lens"],
+                                   batch["tc"][c:c + 1], 3, bits, **kw)
+            assert code == 0 and np.array_equal(one[0], o[c]) and np.array_equal(ls[:, 0], lse[:, c])
