@@ -107,6 +107,7 @@ constexpr float kPastEnd = -0x1p100f;  // column term of a key past the end: exa
 constexpr int kMinUp = -24;            // the candidate's 2^24 at most finite
 constexpr float kPExp = 6.f;        // P holds 2^(x - max + 6)
 constexpr float kMaxSum = 65504.f;  // a tile's sum up to this leaves no term beyond fp16
+constexpr float kFar = 0x1p27f;     // a maximum from which on neighbouring floats are 8 and more apart
 
 struct Params {
   CUtensorMap tq;              // q: [C] rows of H heads x 64 bf16, box of a head and 128 rows
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       const float f = r < mt ? rd[0] : 0.f;  // x = S f (a row past the candidates moves nothing)
       ++qi;
       float m = 0.f, l = 0.f;
-      const uint64_t f2 = f2_pack(f, f);
+      uint64_t f2 = f2_pack(f, f), nm2 = 0ull;  // x - m = S f2 + nm2
       for (int j = 0; j < tiles; ++j, ++g) {
         const int sb = g & 1;
         // S_g's completion covers every MMA issued before it, P_{g-2} V_{g-2} included, so its P
@@ -637,13 +638,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
 #pragma unroll
               for (int e = 0; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
             }
-            mx = __fmaf_ru(mx, f, -kPExp);  // up: no x - m is above kPExp, however coarse floats are there
-            if (j == 0) {
-              m = mx > -INFINITY ? mx : 0.f;
-            } else {
-              const float next = move ? fmaxf(m, mx) : m;
-              const float al = ex2(m - next);
-              m = next;
+            float top = __fmaf_ru(mx, f, -kPExp);  // up: no x - m is above kPExp
+            float fe = f, off = top;
+            if (fabsf(top) >= kFar) {
+              // Rounding up would leave the maximum itself no weight.  S f with a power of two for f, and
+              // the maximum's, are exact, so that it weighs 1; other scores of this size are whole steps
+              // of a float below, in which up to half of f changes what is rounded off anyway.
+              fe = __uint_as_float(__float_as_uint(f) & 0xFF800000u);
+              off = mx * fe;
+              top = mx * f;
+            }
+            const bool take_it = move && (j == 0 ? mx > -INFINITY : top > m);
+            const float al = j == 0 ? 1.f : ex2(take_it ? m - top : 0.f);
+            if (take_it) {
+              m = top;
+              f2 = f2_pack(fe, fe);
+              nm2 = f2_pack(-off, -off);
+            }
+            if (j > 0) {
               l *= al;
               if (!wait_warp(&bars[kPvDone + (sb ^ 1)], par((g - 1) >> 1), abort_flag)) {
                 ok = false;
@@ -662,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
             }
           }
           // P = 2^(x - m), 16 keys at a time with the next ones' load in flight
-          const uint64_t nm2 = f2_pack(-m, -m);
           uint64_t sum2[2] = {0ull, 0ull};
           uint32_t xa[16], xb[16];
           auto part = [&](uint32_t (&s)[16], int c0) {

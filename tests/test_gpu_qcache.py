@@ -975,3 +975,29 @@ def test_a_candidate_beside_an_outlier(G, bits, m, kw):
             one, ls, code = _score(G, batch["qkv"][:, c:c + 1], [0, 1], _dev(batch["cache"]), batch["rows"], batch["lens"],
                                    batch["tc"][c:c + 1], 3, bits, **kw)
             assert code == 0 and np.array_equal(one[0], o[c]) and np.array_equal(ls[:, 0], lse[:, c])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("kw", [{}, WIDE], ids=["few", "many"])
+def test_scores_far_beyond_whole_numbers(G, bits, kw):
+    """Scores q.k from 2^26 to 2^80, between which floats are many log2 units apart: the largest holds
+    the weight, alone or with those equal to it, whichever tile it is in."""
+    batch, values = _batch(66, [(300, 8), (65, 3), (1, 2)], 3, bits)
+    plain = batch["qkv"]
+    for up in (26, 29, 33, 40, 60, 80):
+        batch["qkv"] = plain.copy()
+        batch["qkv"][0] *= np.float32(2.0 ** up)
+        batch["qkv"][0, 5] *= np.float32(2.0 ** -up)  # an ordinary one among them
+        o, lse, _ = _check(G, batch, values, **kw)
+        k, v = (np.asarray(x, np.float64) for x in values[:2])
+        qkv = batch["qkv"].astype(np.float64)
+        for c in (0, 1, 2, 3, 4, 8, 9):
+            u = 0 if c < 8 else 1
+            s = slice(batch["rows"][u], batch["rows"][u] + batch["lens"][u])
+            for h in range(3):
+                x = np.concatenate([k[s, h] @ qkv[0, c, h], [qkv[1, c, h] @ qkv[0, c, h]]])
+                i, second = int(x.argmax()), np.sort(x)[-2]
+                mag = np.abs(qkv[0, c, h]) @ np.abs(np.concatenate([k[s, h], qkv[1, c:c + 1, h]])).max(0)
+                if x[i] - second > 2.0 ** -17 * mag:  # apart by more than fp32 sums may be off
+                    one = v[s, h][i] if i < batch["lens"][u] else qkv[2, c, h]
+                    assert np.array_equal(o[c, h], one), (up, c, h)
