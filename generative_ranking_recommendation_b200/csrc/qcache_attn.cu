@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
   // -------------------------------------------------------------------- one head
   const int h = w.g * kHeads + warp;
   const int g = lane >> 2, t = lane & 3;
-  const float sp2 = a.slope_pos[h] * kLog2e, st2 = a.slope_time[h] * kLog2e;
+  // (the largest slopes stay finite: none times no distance is none)
+  const float sp2 = fminf(a.slope_pos[h] * kLog2e, 3.4e38f), st2 = fminf(a.slope_time[h] * kLog2e, 3.4e38f);
   const float sc2 = a.scale * kLog2e;
 
   // q as the B operand (candidate g), each scaled by its own power of two into fp16's range, and
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kHalfWarps * 16) k_qcached_join(const __grid_c
   const bool on = u < a.B && user_of(P.c, u, c0, m, at, n) && k < m;
   const int splits = on ? min(P.splits, max(1, (min(n, P.c.max_len) + P.chunk - 1) / P.chunk)) : 0;
   const long long ci = c0 + k;
-  const float row_term = on && a.lse ? a.slope_time[h] * kLog2e * (float)(a.ts[ci] - a.ts[c0]) : 0.f;
+  const float row_term = on && a.lse ? fminf(a.slope_time[h] * kLog2e, 3.4e38f) * (float)(a.ts[ci] - a.ts[c0]) : 0.f;
   grid_wait();  // the ranges are there
 
   const float* src = P.part + (ci * a.H + h) * kQPart;

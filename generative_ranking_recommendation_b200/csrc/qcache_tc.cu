@@ -36,6 +36,7 @@
 #include <cuda_fp16.h>
 
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -103,8 +104,12 @@ constexpr uint32_t kIdescPV = idesc_f16(BM, kQDh, 1);
 // far below the largest keeps its bits down to 2^-25 (4 bits) or 2^-30 (8 bits) of it.
 template <int FMT>
 constexpr int kUp = FMT == GENRANK_QCACHE_INT4 ? 9 : 6;
-constexpr float kPastEnd = -0x1p100f;  // column term of a key past the end: exact in bf16, and with
-constexpr int kMinUp = -24;            // the candidate's 2^24 at most finite
+// Scores leave the MMA as x / (f 2^up): f in [1/2, 1) and a whole exponent fe make scale log2 e =
+// f 2^fe, and 2^up is the candidate's, with fe in it.  A key's column term is its bias over f, down to
+// kLowestBias; of a key past the end it is kPastEnd, which no sum of scores reaches.  Both are exact in
+// bf16, and with the candidate's 2^26 at most finite.
+constexpr float kPastEnd = -0x1p100f, kLowestBias = -0x1p98f;
+constexpr int kMinUp = -26;
 constexpr float kPExp = 6.f;        // P holds 2^(x - max + 6)
 constexpr float kMaxSum = 65504.f;  // a tile's sum up to this leaves no term beyond fp16
 constexpr float kFar = 0x1p27f;     // a maximum from which on neighbouring floats are 8 and more apart
@@ -115,6 +120,8 @@ struct Params {
   QcachedAttnArgs c;
   int ctiles, splits, chunk;
   unsigned items;
+  float f, f_inv;  // scale log2 e = f 2^fe
+  int fe;
   float* part;  // [splits][C][H][kQPart], or null
 };
 
@@ -279,6 +286,8 @@ GR_DEVICE uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// A slope in log2 units (the largest stay finite: none times no distance is none)
+GR_DEVICE float slope_log2(float s) { return fminf(s * kLog2e, 3.4e38f); }
 GR_DEVICE float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // e in [-126, 127]
 
 // ------------------------------------------------------------------------------------------
@@ -482,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       if (!rec) break;
       const Item& it = *rec;
       const float down = pow2(-(side == 0 ? it.ke : it.ve));
-      const float sp2 = a.slope_pos[it.h] * kLog2e, st2 = a.slope_time[it.h] * kLog2e;
-      const float inv_sl2 = 1.f / sl2;
+      const float sp2 = slope_log2(a.slope_pos[it.h]), st2 = slope_log2(a.slope_time[it.h]);
+      const float f_inv = P.f_inv;
       bool bad_time = false, bad_pos = false;
       const int tiles = it.tiles, rows = it.rows, n1 = it.n + 1, h = it.h;
       const long long t_ref = it.t_ref, t_min = it.t_min;
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           bad_time |= on && tj > t_min;
           bad_pos |= on && (tail.z < 0 || tail.z > n1);
           const float dp = (float)min(tail.z - n1, 0), dt = (float)min(tj - t_ref, 0ll);
-          term4 = bf16_parts(on ? fmaf(sp2, dp, st2 * dt) * inv_sl2 : kPastEnd);
+          term4 = bf16_parts(on ? fmaxf(fmaf(sp2, dp, st2 * dt) * f_inv, kLowestBias) : kPastEnd);
         }
         // (a K buffer is free after its S, long before the V buffer of the same tile)
         if (!wait_warp(&bars[(side == 0 ? kKEmpty : kVEmpty) + st], par(g / kStages) ^ 1u, abort_flag)) {
@@ -738,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
     auto write_q = [&]() -> bool {  // Q of the qi-th item
       const Item& nx = *nxp;
       const int qb = qi & 1;
-      const float term = a.slope_time[nx.h] * kLog2e * (float)(a.ts[nx.cb + min(r, nx.mt - 1)] - nx.t_ref);
+      const float term = slope_log2(a.slope_time[nx.h]) * (float)(a.ts[nx.cb + min(r, nx.mt - 1)] - nx.t_ref);
       const __nv_bfloat16* k = (const __nv_bfloat16*)a.k + nx.h * kQDh + 8 * ch;
       auto load_k = [&](int i) {
         return __ldg(reinterpret_cast<const uint4*>(
@@ -778,8 +787,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         // q = q' 2^qe, q' below 2 (and smaller where all scores are: its 2^-25 then stands for
         // 2^-43 of a score)
         int qe = min(max((int)(max(top & 0xFFFFu, top >> 16) >> 7) - 127, -126), 126);
-        qe = max(qe, min(kMinUp - nx.ke, 126));
-        const float qd = pow2(-qe);
+        qe = max(qe, kMinUp - P.fe - nx.ke);
+        const float qd = qe <= 126 ? pow2(-qe) : 0.f;
         float f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f2_unpack(f2_mul(f2[e], f2_pack(qd, qd)), f[2 * e], f[2 * e + 1]);
@@ -795,11 +804,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         }
       }
       if (32 * w4 < nx.mt) {
-        const int up = min(own_qe + nx.ke, 126);
-        const uint32_t one = __float_as_uint(pow2(max(-up, -126))) >> 16;
+        const int up = min(max(own_qe + nx.ke + P.fe, kMinUp), 126);  // (of rows past the candidates as well)
+        const uint32_t one = __float_as_uint(pow2(-up)) >> 16;
         reinterpret_cast<uint4*>(smem + kOffQA + qb * kQABytes)[r] = make_uint4(one | (one << 16), one, 0u, 0u);
         float* rd = rowdata + qb * 4 * BM + r;
-        rd[0] = sl2 * pow2(max(up, -126));
+        rd[0] = P.f * pow2(up);
         rd[BM] = fmaf(own_dot, sl2, term);
         rd[2 * BM] = term;
       }
@@ -965,6 +974,8 @@ int launch_qcached_tc(const QcachedAttnArgs& c, int ctiles, int splits, int chun
   P.chunk = chunk;
   P.items = (unsigned)((long long)c.a.B * ctiles * splits * c.a.H);
   P.part = part;
+  P.f = (float)frexp((double)c.a.scale * (double)kLog2e, &P.fe);
+  P.f_inv = 1.f / P.f;
   return c.format == GENRANK_QCACHE_INT8 ? qtc::launch<GENRANK_QCACHE_INT8>(P, st)
                                          : qtc::launch<GENRANK_QCACHE_INT4>(P, st);
 }

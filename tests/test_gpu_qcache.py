@@ -1001,3 +1001,39 @@ def test_scores_far_beyond_whole_numbers(G, bits, kw):
                 if x[i] - second > 2.0 ** -17 * mag:  # apart by more than fp32 sums may be off
                     one = v[s, h][i] if i < batch["lens"][u] else qkv[2, c, h]
                     assert np.array_equal(o[c, h], one), (up, c, h)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("kw", [WIDE, {}], ids=["many", "few"])
+@pytest.mark.parametrize("scale,slope", [(2.0 ** -100, 0.0), (2.0 ** -140, 0.02), (2.0 ** -60, 1e-30), (2.0 ** -100, 3e38),
+                                         (0.125, 3e38), (0.125, 2e30), (2.0 ** 40, 0.5)])
+def test_scales_and_slopes_of_any_size(G, bits, kw, scale, slope):
+    """Scores that vanish, biases beyond fp32: histories that end inside a tile of either form."""
+    H, users = 2, [(70, 5), (33, 3), (1, 2)]
+    batch, values = _batch(62, users, H, bits)
+    k, v, pos, ts = values
+    last = batch["rows"][0] + 69
+    ts[last] = batch["tc"][0]  # no time between the candidates and this row
+    batch["cache"] = oracle.qcache_rows(k, v, pos, ts, bits)
+    if scale > 1.0:
+        batch["qkv"][0] *= np.float32(2.0 ** -40)
+    C, d = 10, H * 64
+    x = _dev(batch["qkv"].transpose(1, 0, 2, 3).reshape(C, 3 * d), torch.bfloat16)
+    mc, ml = kw.get("max_cand", 5), kw.get("max_len", 70)
+    ws = torch.empty(max(16, G.attn_qcached_workspace_size(3, C, H, 64, mc, ml)), dtype=torch.uint8, device="cuda")
+    o = torch.empty(C, d, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(H, C, dtype=torch.float32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for sp, st in (([slope, 0.0], [0.0, 0.0]), ([0.0, 0.0], [slope, slope / 1024])):
+        sp, st = ([float(np.float32(s)) for s in z] for z in (sp, st))
+        G.attn_fwd_qcached(_dev(batch["coff"], torch.int32), mc, x, x[:, d:], x[:, 2 * d:], 3 * d, _dev(batch["cache"]),
+                           _dev(batch["rows"], torch.int64), _dev(batch["lens"], torch.int32), ml, _dev(batch["tc"], torch.int64),
+                           H, 64, sp, st, scale, o, d, lse, ws, _fmt(G, bits), err)
+        assert G.check_error(err) == 0
+        want, wl, A, S = oracle.attention_fwd_qcached(*batch["qkv"].astype(np.float64), batch["coff"], k, v, batch["rows"],
+                                                      batch["lens"], pos, ts, batch["tc"], sp, st, scale)
+        e = 2.0 ** -18 * S + 2.0 ** -19
+        got = o.double().cpu().numpy().reshape(C, H, 64)
+        tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -11 + 2 * e.T[:, :, None]) + 70 * 2.0 ** -30 * np.abs(v).max()
+        assert np.all(np.abs(got - want) <= tol), np.nanmax(np.abs(got - want) / tol)
+        assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= e + 2.0 ** -22 * np.abs(wl))
