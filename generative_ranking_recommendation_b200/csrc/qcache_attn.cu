@@ -5,8 +5,10 @@
 //   s_cj = scale q_c.k_j - m_h |n + 1 - p_j| - m_t,h |t_c - t_j|,   s_cc = scale q_c.k_c
 // With k_j = s_j c_j (whole codes c_j, one scale a token and head) the score is
 // (q_c.c_j) (s_j scale log2 e) + col_j, where col_j = log2 e (m_h (p_j - n - 1) +
-// m_t,h (t_j - t_0)) is the key's part of the bias against the user's first candidate time t_0
-// and the row's part, log2 e m_t,h (t_c - t_0), cancels in the softmax.  Codes of at most 7 bits
+// m_t,h (t_j - t_0)) is the key's part of the bias against t_0, the earliest time of the block's
+// candidates, and the row's part, log2 e m_t,h (t_c - t_0) >= 0, is taken off the cached rows'
+// maximum when the candidate itself joins them: only a candidate whose history has no weight then
+// sees large numbers cancel.  Codes of at most 7 bits
 // are exact in fp16, so q.c has exact products and fp32 sums: no key is ever rounded.
 //
 // One pass over the rows with the running maximum and sum of an online softmax:
@@ -32,6 +34,8 @@
 // the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 84 us).
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "host_util.h"
 #include "kernels.h"
@@ -47,6 +51,7 @@ constexpr int kMaxThreads = (kHeads + 1) * 32;  // the heads' warps and the one 
 constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
 constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
 constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
+constexpr float kHighest = 1e38f;  // of a candidate's time term
 
 struct Params {
   QcachedAttnArgs c;
@@ -258,7 +263,6 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
   }
   __syncthreads();
 
-  const long long t_ref = a.ts[c0];
   if (warp == (int)blockDim.x / 32 - 1) {
     // ------------------------------------------------------------------ copies and distances
     const uint8_t* src = c.cache + (at + lo) * (long long)L.bytes;
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
         const bool on = r < hi - lo - i * kRows;
         bad_time |= on && tj > t_min;
         bad_pos |= on && (tail.z < 0 || tail.z > n + 1);
-        gaps[st][r] = on ? make_float4((float)min(tail.z - (n + 1), 0), (float)min(tj - t_ref, 0ll), 0.f, 0.f)
+        gaps[st][r] = on ? make_float4((float)min(tail.z - (n + 1), 0), (float)min(tj - t_min, 0ll), 0.f, 0.f)
                          : make_float4(0.f, 0.f, -INFINITY, 0.f);
         // rows past the end (of the block's last tile) hold what the stage held before: any codes
         // are finite, but a scale might not be
@@ -379,12 +383,15 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
     for (int e = 0; e < 2; ++e) self[e] = __shfl_sync(0xffffffffu, dot * sc2, 4 * (2 * t + e));
   }
   float row_term[2], mx[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const long long tc = a.ts[cb + min(2 * t + e, mt - 1)];
-    row_term[e] = st2 * (float)(tc - t_ref);
-    self[e] += row_term[e];
-    mx[e] = fmaxf(self[e], kLowest);
+  {
+    const long long t0 = a.ts[cb + min(2 * t, mt - 1)], t1 = a.ts[cb + min(2 * t + 1, mt - 1)];
+    long long t_min = min(t0, t1);
+    t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, 1));
+    t_min = min(t_min, __shfl_xor_sync(0xffffffffu, t_min, 2));
+    row_term[0] = fminf(st2 * (float)(t0 - t_min), kHighest);
+    row_term[1] = fminf(st2 * (float)(t1 - t_min), kHighest);
+    // the maximum starts where the candidate's own score is
+    for (int e = 0; e < 2; ++e) mx[e] = fmaxf(self[e] + row_term[e], kLowest);
   }
   uint64_t sum2 = 0ull;  // the lane's two candidates: (+0, +0)
 
@@ -532,8 +539,14 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
       x[2 * d] = o[d][e] * up;
       x[2 * d + 1] = o[d][e + 2] * up;
     }
+    // rows without weight (l = 0) say nothing about where their maximum is
+    float top = l == 0.f ? -FLT_MAX : mx[e] - row_term[e];
     if (w.s == 0) {  // the candidate itself
-      const float ps = ex2(self[e] - mx[e]);
+      const float next = fmaxf(top, self[e]), ph = ex2(top - next), ps = ex2(self[e] - next);
+      top = next;
+      l *= ph;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) x[d] *= ph;
       float vf[8];
       Elem<__nv_bfloat16>::unpack(
           __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.v + ci * a.tok_stride + h * kQDh + 8 * g)), vf);
@@ -545,13 +558,13 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
       float* dst = P.part + (((long long)w.s * a.T + ci) * a.H + h) * kQPart;
 #pragma unroll
       for (int d = 0; d < 8; d += 2) *reinterpret_cast<float2*>(dst + 8 * g + d) = make_float2(x[d], x[d + 1]);
-      if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(mx[e], l);
+      if (g == 0) *reinterpret_cast<float2*>(dst + kQDh) = make_float2(top, l);
     } else {
       const float inv = 1.f / l;
 #pragma unroll
       for (int d = 0; d < 8; ++d) x[d] *= inv;
       *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + 8 * g) = Elem<__nv_bfloat16>::pack(x);
-      if (a.lse && g == 0) a.lse[(long long)h * a.T + ci] = (mx[e] + log2f(l) - row_term[e]) * kLn2;
+      if (a.lse && g == 0) a.lse[(long long)h * a.T + ci] = (top + log2f(l)) * kLn2;
     }
   }
 }
@@ -576,7 +589,6 @@ __global__ void __launch_bounds__(kHalfWarps * 16) k_qcached_join(const __grid_c
   const bool on = u < a.B && user_of(P.c, u, c0, m, at, n) && k < m;
   const int splits = on ? min(P.splits, max(1, (min(n, P.c.max_len) + P.chunk - 1) / P.chunk)) : 0;
   const long long ci = c0 + k;
-  const float row_term = on && a.lse ? fminf(a.slope_time[h] * kLog2e, 3.4e38f) * (float)(a.ts[ci] - a.ts[c0]) : 0.f;
   grid_wait();  // the ranges are there
 
   const float* src = P.part + (ci * a.H + h) * kQPart;
@@ -627,7 +639,7 @@ __global__ void __launch_bounds__(kHalfWarps * 16) k_qcached_join(const __grid_c
   const float inv = 1.f / l;
   *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + ci * a.o_stride + h * kQDh + d) =
       make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-  if (a.lse && lane == 0) a.lse[(long long)h * a.T + ci] = (top + log2f(l) - row_term) * kLn2;
+  if (a.lse && lane == 0) a.lse[(long long)h * a.T + ci] = (top + log2f(l)) * kLn2;
 }
 
 struct Plan {

@@ -112,6 +112,7 @@ constexpr float kPastEnd = -0x1p100f, kLowestBias = -0x1p98f;
 constexpr int kMinUp = -26;
 constexpr float kPExp = 6.f;        // P holds 2^(x - max + 6)
 constexpr float kMaxSum = 65504.f;  // a tile's sum up to this leaves no term beyond fp16
+constexpr float kHighest = 1e38f;   // of a candidate's time term
 constexpr float kFar = 0x1p27f;     // a maximum from which on neighbouring floats are 8 and more apart
 
 struct Params {
@@ -131,9 +132,8 @@ struct Item {
   int n, rows, tiles;    // the user's rows, the item's, and their tiles (-1: no more items)
   int at;                // the item's first cache row
   int ke, ve;            // powers of two, 2^kUp of which are above every K and V scale
-  long long t_ref;       // time of the user's first candidate, the origin of the bias
-  long long t_min;       // earliest time of the item's candidates
-  int c0, pad;
+  long long t_min;       // earliest time of the item's candidates, the origin of the bias
+  int pad[4];
 };
 static_assert(sizeof(Item) == 64, "a record");
 
@@ -161,7 +161,6 @@ GR_DEVICE Item next_item(const Params& P, const QRow& L, unsigned& w) {
     const bool good = b >= 0 && e >= b && e <= c.a.T && it.n >= 0 && at >= 0 && it.n <= c.R && at <= c.R - it.n;
     if (lane == 0 && it.h == 0 && it.s == 0 && (!good || e - b > c.max_cand || it.n > c.max_len))
       flag(c.a.err, GENRANK_DERR_LAYOUT);
-    it.c0 = b;
     it.cb = b + ct * BM;
     it.mt = min(min(e - b, c.max_cand) - ct * BM, BM);
     const int lo = it.s * P.chunk;
@@ -173,7 +172,6 @@ GR_DEVICE Item next_item(const Params& P, const QRow& L, unsigned& w) {
     // its largest scales and its candidates' earliest time
     const uint8_t* src = c.cache + (at + lo) * L.bytes + L.scales + 4 * it.h;
     float kmax = 0.f, vmax = 0.f;
-    it.t_ref = c.a.ts[b];
     it.t_min = LLONG_MAX;
 #pragma unroll
     for (int r = 0; r < BM; r += 32) it.t_min = min(it.t_min, (long long)c.a.ts[it.cb + min(r + lane, it.mt - 1)]);
@@ -495,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       const float f_inv = P.f_inv;
       bool bad_time = false, bad_pos = false;
       const int tiles = it.tiles, rows = it.rows, n1 = it.n + 1, h = it.h;
-      const long long t_ref = it.t_ref, t_min = it.t_min;
+      const long long t_min = it.t_min;
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j, ++g) {
         const int st = g % kStages, sl = g % R::kSlots;
@@ -513,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           const long long tj = (long long)(((uint64_t)(uint32_t)tail.y << 32) | (uint32_t)tail.x);
           bad_time |= on && tj > t_min;
           bad_pos |= on && (tail.z < 0 || tail.z > n1);
-          const float dp = (float)min(tail.z - n1, 0), dt = (float)min(tj - t_ref, 0ll);
+          const float dp = (float)min(tail.z - n1, 0), dt = (float)min(tj - t_min, 0ll);
           term4 = bf16_parts(on ? fmaxf(fmaf(sp2, dp, st2 * dt) * f_inv, kLowestBias) : kPastEnd);
         }
         // (a K buffer is free after its S, long before the V buffer of the same tile)
@@ -747,7 +745,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
     auto write_q = [&]() -> bool {  // Q of the qi-th item
       const Item& nx = *nxp;
       const int qb = qi & 1;
-      const float term = slope_log2(a.slope_time[nx.h]) * (float)(a.ts[nx.cb + min(r, nx.mt - 1)] - nx.t_ref);
+      const float term =
+          fminf(slope_log2(a.slope_time[nx.h]) * (float)(a.ts[nx.cb + min(r, nx.mt - 1)] - nx.t_min), kHighest);
       const __nv_bfloat16* k = (const __nv_bfloat16*)a.k + nx.h * kQDh + 8 * ch;
       auto load_k = [&](int i) {
         return __ldg(reinterpret_cast<const uint4*>(
@@ -809,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
         reinterpret_cast<uint4*>(smem + kOffQA + qb * kQABytes)[r] = make_uint4(one | (one << 16), one, 0u, 0u);
         float* rd = rowdata + qb * 4 * BM + r;
         rd[0] = P.f * pow2(up);
-        rd[BM] = fmaf(own_dot, sl2, term);
+        rd[BM] = own_dot * sl2;
         rd[2 * BM] = term;
       }
       fence_proxy_async_smem();
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
       if (!wait_warp(&bars[kOFull], par(done), abort_flag)) break;
       tc_fence_after();
       const float* rd = rowdata + qb * 4 * BM + r;
-      const float m = rd[0], own = rd[BM], l = rd[3 * BM];
+      const float m = rd[0] - rd[2 * BM], own = rd[BM], l = rd[3 * BM];
       const bool row_ok = r < it.mt;
       const long long ci = it.cb + min(r, it.mt - 1);
       // the candidate itself joins where the item is the first range
@@ -897,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qcached_tc(const __grid_constan
           const int row = 32 * w4 + 4 * k + sub;
           if (row < it.mt) *reinterpret_cast<uint4*>(out + (long long)row * a.o_stride) = *chunk_at(stage, 4 * k + sub, ch);
         }
-        if (row_ok && a.lse) a.lse[(long long)it.h * a.T + ci] = (top + log2f(total) - rd[2 * BM]) * kLn2;
+        if (row_ok && a.lse) a.lse[(long long)it.h * a.T + ci] = (top + log2f(total)) * kLn2;
       }
       give_back(done);
       if (!more) break;

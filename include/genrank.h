@@ -392,8 +392,8 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  * GENRANK_DERR_LAYOUT (a user's offsets or rows outside their arrays: the user is left out;
  * more than max_cand candidates or max_len rows: the rest is left out), GENRANK_DERR_TS_ORDER
  * (a cached time after a candidate's), GENRANK_DERR_POS_RANGE (a cached position outside
- * [0, n_u + 1]); in the last two cases a distance below zero (in time: from the user's first
- * candidate) counts as zero.
+ * [0, n_u + 1]); in the last two cases a distance below zero (in time: from the earliest of the
+ * candidates that are computed together) counts as zero.
  * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, each head of
  * each candidate scaled by a power of two of its own: exact down to 2^-17 of its largest element,
  * 2^-25 of that below; softmax weights are rounded to fp16's 11 bits.  Under the same bounds a

@@ -1037,3 +1037,36 @@ def test_scales_and_slopes_of_any_size(G, bits, kw, scale, slope):
         tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -11 + 2 * e.T[:, :, None]) + 70 * 2.0 ** -30 * np.abs(v).max()
         assert np.all(np.abs(got - want) <= tol), np.nanmax(np.abs(got - want) / tol)
         assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= e + 2.0 ** -22 * np.abs(wl))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("users,kw", [([(200, 8), (90, 3)], {}), ([(200, 8), (90, 3)], WIDE), ([(3000, 5)], {}),
+                                      ([(3000, 60)], dict(max_cand=900))], ids=["few", "many", "few-ranges", "many-ranges"])
+def test_candidates_far_apart_in_time(G, bits, users, kw):
+    """A week between a user's candidates, the first one the latest, and slopes by which the history
+    matters to the early ones: no score is the difference of two large numbers, and the order of the
+    candidates does not matter.  A bias of x nats weighs e^-x, so that only those up to 64 count in
+    the LSE, each rounded to 2^-22 of itself."""
+    H = 2
+    batch, values = _batch(63, users, H, bits)
+    k, v, pos, ts = values
+    c0 = np.array(batch["coff"])
+    slopes = ([0.0, 0.0], [1.0 / 16, 1.0 / 64])
+    for u, (n, m) in enumerate(users):
+        t0 = 1_700_000_000
+        ts[batch["rows"][u]:batch["rows"][u] + n] = t0 - 3 * np.arange(n)[::-1] - 5
+        tc = t0 + np.arange(m) * 7
+        tc[0] = t0 + 7 * 86400
+        tc[m // 2] = t0 + 3 * 86400
+        batch["tc"][c0[u]:c0[u + 1]] = tc
+    batch["cache"] = oracle.qcache_rows(k, v, pos, ts, bits)
+    o, lse, _ = _check(G, batch, values, slopes=slopes, **kw)
+    want, wl, A, S = oracle.attention_fwd_qcached(*batch["qkv"].astype(np.float64), batch["coff"], k, v, batch["rows"],
+                                                  batch["lens"], pos, ts, batch["tc"], *slopes, 0.125)
+    err = np.abs(lse - wl)
+    tol = 2.0 ** -18 * S + 2.0 ** -19 + 2.0 ** -22 * (np.abs(wl) + 64)
+    assert np.all(err <= tol), np.max(err / tol)
+    turn = np.concatenate([np.arange(c0[u], c0[u + 1])[::-1] for u in range(len(users))])
+    b = dict(batch, qkv=batch["qkv"][:, turn], tc=batch["tc"][turn])
+    back, lback, _ = _check(G, b, values, slopes=slopes, **kw)
+    assert np.array_equal(back, o[turn]) and np.array_equal(lback, lse[:, turn])
