@@ -48,8 +48,11 @@ constexpr int kHeads = 8;    // heads of a block, one warp each
 constexpr int kCands = 8;    // candidates of a block
 constexpr int kStages = 3;   // tiles in flight
 constexpr int kMaxThreads = (kHeads + 1) * 32;  // the heads' warps and the one that copies
-constexpr float kSlack = 8.f;    // a score may pass the running maximum by this (log2)
-constexpr int kVExp = 7;         // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
+// P s enters the second product in fp16, s over the largest V scale so far: its 11 bits are whole down
+// to P s = 2^-25 of that, its smallest numbers 2^-35.  (A slack of 8 and 2^7 lost bits from 2^-21 on;
+// the more frequent moves cost ragged batches of up to 33 candidates 1 to 2 %, one candidate nothing.)
+constexpr float kSlack = 4.f;  // a score may pass the running maximum by this (log2)
+constexpr int kVExp = 11;      // P s <= 2^(kSlack + kVExp) = 2^15 < 65504
 constexpr float kLowest = -1e30f;  // a maximum to start from when the own score is -inf
 constexpr float kHighest = 1e38f;  // of a candidate's time term
 

@@ -397,8 +397,10 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  * Scores, softmax statistics and sums are fp32.  q enters the tensor cores in fp16, each head of
  * each candidate scaled by a power of two of its own: exact down to 2^-17 of its largest element,
  * 2^-25 of that below; softmax weights are rounded to fp16's 11 bits.  Under the same bounds a
- * candidate's result is the same bits whatever other candidates there are.  With many candidates, rows whose scale is below 2^-25
- * (int4; 2^-30 int8) of the largest of the head's history lose low bits. */
+ * candidate's result is the same bits whatever q, key and value the other candidates have.  Value
+ * scales far below the largest of a head's history lose low bits: with few candidates where weight
+ * times scale is below 2^-25 of the largest scale (a row is off by 2^-35 of that times its code at
+ * most), with many where the scale, of keys as well, is below 2^-25 (int4) or 2^-30 (int8). */
 int genrank_attn_fwd_qcached(int B, int64_t C, const int32_t *cand_offsets, int max_cand,
                              const void *q_c, const void *k_c, const void *v_c,
                              int64_t cand_stride, const void *cache, int64_t R,

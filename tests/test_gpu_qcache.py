@@ -1070,3 +1070,34 @@ def test_candidates_far_apart_in_time(G, bits, users, kw):
     b = dict(batch, qkv=batch["qkv"][:, turn], tc=batch["tc"][turn])
     back, lback, _ = _check(G, b, values, slopes=slopes, **kw)
     assert np.array_equal(back, o[turn]) and np.array_equal(lback, lse[:, turn])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("kw", [{}, WIDE], ids=["few", "many"])
+def test_value_scales_far_below_the_largest(G, bits, kw):
+    """One row of large values and no weight before two of small ones.  Few candidates: a weight times
+    its value scale enters the product in fp16 under 2^11 over a power of two at most twice the
+    largest scale, where half a step of the smallest numbers is 2^-25, so that a row is off by 2^-35
+    of the largest value at most.  Many: value scales down to 2^-25 (8 bits: 2^-30) of the largest
+    are exact; heads' scales differ by up to a factor of 6 here."""
+    H, n = 4, 3
+    for down in (15, 20, 28) if not kw else (15, 20, 22 if bits == 4 else 27):
+        batch, _ = _batch(64, [(n, 8)], H, bits, qscale=0.5)
+        r, R = np.random.default_rng(64), len(batch["cache"])
+        k, v = _kv(r, R, H), _kv(r, R, H)
+        pos, ts = np.zeros(R, np.int64), np.zeros(R, np.int64)
+        at = int(batch["rows"][0])
+        pos[at + 1:at + n], ts[at:at + n] = n + 1, batch["tc"][0] - 9
+        v[at + 1:at + n] *= np.float32(2.0 ** -down)
+        batch["qkv"][2] *= np.float32(2.0 ** -down)
+        batch["cache"] = oracle.qcache_rows(k, v, pos, ts, bits)
+        slopes = ([40.0] * H, [0.0] * H)  # 160 nats for the first row, none for the others
+        o, _, code = _score(G, batch["qkv"], batch["coff"], _dev(batch["cache"]), batch["rows"], batch["lens"], batch["tc"], H, bits,
+                            slopes=slopes, **kw)
+        assert code == 0
+        want, _, A, S = oracle.attention_fwd_qcached(*batch["qkv"].astype(np.float64), batch["coff"], oracle.qcache_values(k, bits),
+                                                     oracle.qcache_values(v, bits), batch["rows"], batch["lens"], pos, ts,
+                                                     batch["tc"], *slopes, 0.125)
+        e = (2.0 ** -18 * S + 2.0 ** -19).T[:, :, None]
+        tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -11 + 2 * e) + (0.0 if kw else (n - 1) * 2.0 ** -35 * np.abs(v[at]).max())
+        assert np.all(np.abs(o - want) <= tol), (down, np.max(np.abs(o - want) / tol))
