@@ -407,17 +407,22 @@ def _mat(what, name, t, dev, dtype, rows, stride, width):
 
 @functools.lru_cache(maxsize=256)
 def _slopes(xs):
+    """xs: a tuple of Python floats (a tensor's element would be kept by its identity)."""
     return (ctypes.c_float * len(xs))(*xs)
 
 
 @functools.lru_cache(maxsize=1024)
-def qcache_row_bytes(H, dh, fmt) -> int:
-    """Bytes of one row (one token) of a quantised history cache: allocate it as a uint8 tensor
-    [rows, qcache_row_bytes(H, dh, fmt)].  fmt: QCACHE_INT8 or QCACHE_INT4."""
-    n = int(lib().genrank_qcache_row_bytes(int(H), int(dh), int(fmt)))
+def _row_bytes(H, dh, fmt):
+    n = int(lib().genrank_qcache_row_bytes(H, dh, fmt))
     if n == 0:
         raise GenRankError(f"qcache: unsupported H={H}, dh={dh} or format {fmt}")
     return n
+
+
+def qcache_row_bytes(H, dh, fmt) -> int:
+    """Bytes of one row (one token) of a quantised history cache: allocate it as a uint8 tensor
+    [rows, qcache_row_bytes(H, dh, fmt)].  fmt: QCACHE_INT8 or QCACHE_INT4."""
+    return _row_bytes(int(H), int(dh), int(fmt))
 
 
 def _cache(what, cache, dev, H, dh, fmt):
@@ -496,7 +501,8 @@ def attn_fwd_qcached(cand_offsets, max_cand, q_c, k_c, v_c, cand_stride, cache, 
         _vec(what, "rows", rows, dev, torch.int64, B),
         _vec(what, "cache_len", cache_len, dev, torch.int32, B), int(max_len),
         _vec(what, "ts_cand", ts_cand, dev, torch.int64, C), int(fmt), int(H), int(dh),
-        _slopes(tuple(slope_pos)), _slopes(tuple(slope_time)), float(scale), _dtype_code(q_c),
+        _slopes(tuple(map(float, slope_pos))), _slopes(tuple(map(float, slope_time))), float(scale),
+        _dtype_code(q_c),
         _mat(what, "o", o, dev, dt, C, o_stride, width), int(o_stride),
         None if lse is None else _vec(what, "lse", lse, dev, torch.float32, H * C),
         None if ws is None else _vec(what, "ws", ws, dev, torch.uint8, 0),

@@ -1101,3 +1101,13 @@ def test_value_scales_far_below_the_largest(G, bits, kw):
         e = (2.0 ** -18 * S + 2.0 ** -19).T[:, :, None]
         tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -11 + 2 * e) + (0.0 if kw else (n - 1) * 2.0 ** -35 * np.abs(v[at]).max())
         assert np.all(np.abs(o - want) <= tol), (down, np.max(np.abs(o - want) / tol))
+
+
+def test_slopes_changed_in_place(G):
+    """Slopes given as tensors, changed between two calls: the second call sees the new ones."""
+    batch, values = _batch(65, [(60, 2)], 2, 4)
+    slopes = [[torch.tensor(0.5), torch.tensor(0.25)], [torch.tensor(0.0), torch.tensor(0.0)]]
+    for x in (0.5, 0.01, 3.0):
+        for t in slopes[0]:
+            t.fill_(x)
+        _check(G, batch, values, slopes=slopes)
