@@ -12,8 +12,12 @@
 //
 // Both kernels move bytes and are bound by HBM.  A warp takes a run of consecutive rows; 8
 // lanes hold one head (16 bytes of bf16 a lane), so the maximum is three shuffles.  1024 users x
-// 480 rows of 8 heads, bf16 and 4 bits: append 264 us (4.9 TB/s), read 246 (5.2); 256 users of up to
-// 2048 rows read to fp32 238 us (5.5 TB/s).
+// 480 rows of 8 heads, bf16: append 244 us (5.3 TB/s) to 4 bits and 258 (6.0) to 8, read 254 (5.1) and
+// 284 (5.4); with 256 rows of nobody behind each history, where whole warps have no row to copy,
+// append 284 and 283, read 303 and 328.  256 users of up to 2048 rows read to fp32 230 us (5.6 TB/s).
+// More than 8 heads take the pieces one after the other, with two blocks an SM: 512 x 480 rows of 16
+// heads 273 us (4.7 TB/s) to 4 bits and 299 (5.1) to 8.  Of the forms for up to 8 heads, held to 64
+// registers, three spill: bf16 to 4 bits 16 bytes, fp32 to 4 bits 52, fp32 to 8 bits 132.
 #include "common.cuh"
 #include "host_util.h"
 #include "kernels.h"

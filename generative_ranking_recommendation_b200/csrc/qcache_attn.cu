@@ -29,9 +29,10 @@
 //     candidate's own score: most tiles take one vote and no shuffles.
 //   * Short of blocks, the history is cut into ranges; the ranges' (max, sum, O) in fp32 are
 //     joined by a second kernel, always in the same order.
-// Bound: with one candidate the copies, at 256 users x 4096 rows of 8 heads 150 us for int4 rows
-// (587 MB, 3.9 TB/s; the copies alone take 117) and 200 us for int8 (1124 MB, 5.6 TB/s); with more
-// the unpacking, which every 8 candidates repeat (32 candidates, 480 rows: 84 us).
+// Bound: with one candidate the copies and the unpacking, at 256 users x 4096 rows of 8 heads 152 us
+// for int4 rows (587 MB, 3.9 TB/s; the copies alone take 117), and the copies for int8, 203 us (1124
+// MB, 5.5 TB/s); with more the unpacking, which every 8 candidates repeat (256 users x 480 rows x 32
+// candidates: 90 us).
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -574,8 +575,8 @@ __global__ void __launch_bounds__(kMaxThreads, SUB == 1 ? 3 : 2) k_qcached(const
 
 // Joins the ranges of a candidate and head: `ways` half-warps, four dimensions a lane, each take
 // every ways-th range, then the first adds up what they found.  The order of the sums depends on the
-// number of ranges alone.  What it takes is latency (4 users' 8 candidates of 8 heads in 37 ranges,
-// 2.5 MB), so it is launched while the ranges are worked on and loads four of them at once.
+// number of ranges alone.  What it takes is latency (4 users' 8 candidates of 8 heads in 74 ranges,
+// 5 MB), so it is launched while the ranges are worked on and loads four of them at once.
 constexpr int kHalfWarps = 16;
 __global__ void __launch_bounds__(kHalfWarps * 16) k_qcached_join(const __grid_constant__ Params P) {
   __shared__ __align__(16) float parts[kHalfWarps][kQDh];
@@ -650,12 +651,19 @@ struct Plan {
   int groups, ctiles, splits, chunk;
   long long units;  // blocks, or items, of one range
 };
-// From how many candidates a user the tensor-core form runs, and from how many rows for all blocks:
-// at 256 users x 480 rows of 8 heads it takes 98 us for 24 candidates, 100 for 40 and 109 for 96 and
-// 128 (8 bits: 106, 109, 111), the blocks 76 us for 24, 84 for 32, 109 for 40, 129 for 48.  But its
-// item is a long chain (31 us alone for 480 rows), and blocks are faster while they find free SMs:
-// 128 candidates x 480 rows 16 against 25 us for 1 user (7680 rows), 31 against 37 for 16 users (123
-// thousand), 53 against 31 for 32.
+// From how many candidates a user at most the tensor-core form runs, and from how many rows for all
+// blocks.  The bound on candidates is all that the host knows of them, and where they are fewer the
+// blocks save the tiles of 8 that are not there, items of 128 nothing.  As many for each user (256
+// users x 480 rows of 8 heads, 4 / 8 bits, us): blocks 78 / 82 for 24 candidates, 90 / 94 for 32, 111 /
+// 113 for 33, 112 / 116 for 40, 131 / 135 for 41, 166 / 171 for 64; tensor cores 96 / 104, 99 / 105, 100
+// / 106, 101 / 107, 101 / 107, 103 / 109.  Up to as many (300 users of up to 2000 rows, 5 heads, 8
+// bits): blocks 113 for 33, 125 for 40, 138 for 48, 184 for 64; tensor cores 178, 190, 190, 207 (256
+// users of up to 480 rows, 4 bits: 52 for 33, 58 for 40 against 74, 80).  The former ask for 33, the
+// latter for more than 64: a sixth tile of 8 lies between, with which the former lose up to a sixth
+// (1024 users x 33: 389 us against 333) and the latter up to two fifths (at 48).
+// But an item is a long chain (31 us alone for 480 rows), and blocks are faster while they find free
+// SMs: 128 candidates x 480 rows 16 against 25 us for 1 user (7680 rows), 31 against 37 for 16 users
+// (123 thousand), 53 against 31 for 32.
 constexpr int kTcFrom = 41;
 constexpr long long kTcRows = 1 << 17;
 
@@ -664,9 +672,9 @@ constexpr long long kTcRows = 1 << 17;
 // their registers cost warps (32 candidates: 139 us in one tile, 90 us in four).
 // The history is cut into ranges where that fills the 148 SMs better.  In units of a row's time in
 // one of the blocks that share an SM: a block takes its rows and about 100 to start, one that has
-// its SM to itself an eighth longer, and the join costs about 100.  (4 users x 65536 rows of 8 bits:
-// 72 us in 37 ranges, 99 in 18, 103 in 148; 64 users x 4096: 109 us uncut, 69 in 2, 59 in 4, 71 in
-// 16; 128 users x 480: 25 us uncut, 30 in 2.)
+// its SM to itself an eighth longer, and the join costs about 100.  (8 heads, 8 candidates, 8 bits, the
+// count taken first: 4 users x 65536 rows 70 us in 74 ranges, 71 in 37, 103 in 18, 76 in 148; 64 users
+// x 4096: 70 us in 4, 113 uncut, 74 in 2, 82 in 16; 128 users x 480: 29 us uncut, 33 in 2.)
 Plan plan(int B, int H, int max_cand, int max_len) {
   Plan p;
   p.groups = (H + kHeads - 1) / kHeads;
@@ -731,10 +739,13 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   P.chunk = p.chunk;
   P.ways = ways;
   P.part = p.splits > 1 ? (float*)c.a.ws : nullptr;
-  // More blocks than the SMs hold at once, each a whole history: those longer than half the bound go
-  // first, so that no long one begins last (1500 blocks of 0 to 2000 rows: 128 -> 118 us).  The
-  // blocks that have nothing to do in a pass cost 3 ns each, too much for many short histories
-  // (2000 of 0 to 480: 100 -> 106 us).
+  // More blocks than the SMs hold at once (3 of an SM), each a whole history: those longer than half
+  // the bound go first, so that no long one begins last.  What this saves is part of a longest
+  // history's time at the end, about 10 ns a row of the bound; what it costs are the blocks that have
+  // nothing to do in a pass, 3 ns each, whatever the bound: hence blocks against rows.  Once and twice
+  // (us): 1500 blocks of up to 2000 rows 126, 112; 1000 of 2000 202, 191; 3000 of 4000 266, 246; 500 of
+  // 2000 115, 115; beyond the rule 1000 of 480 73, 73, 2000 of
+  // 480 112, 116, 2000 of 1000 195, 193, 3000 of 2000 181, 174.  Histories of one length take the same time either way.
   P.first = (unsigned)(p.units * p.splits);
   const bool twice = !p.tc && p.splits == 1 && p.units > 444 && p.units < c.max_len;
   const unsigned blocks = twice ? 2 * P.first : P.first;

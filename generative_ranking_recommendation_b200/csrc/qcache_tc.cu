@@ -5,10 +5,10 @@
 // of candidates a row of the cache is used often enough that it pays to write its values out as
 // tensor-core operands once per 128 candidates: what bounds the work in the end is one exponential
 // per pair (16 a clock and SM: 512 clocks for 128 x 64 pairs, the products take half of that).
-// Today it is instruction issue: a tile of 128 x 64 pairs takes about 4000 warp instructions, of
-// which 0.67 a clock and scheduler are issued by the 27 warps that fit an SM.  1024 users x 480 rows
-// x 256 candidates x 8 heads of 4 bits: 694 us (5.3 ns a tile over the GPU; the exponentials alone
-// 240 us); 64 x 480 x 1024 x 16 heads of 8 bits: 366 us.
+// Today it is instruction issue: a tile of 128 x 64 pairs takes 3770 warp instructions (8 bits: 3490),
+// of which 0.65 (0.55) a clock and scheduler are issued by the 27 warps that fit an SM.  1024 users x
+// 480 rows x 256 candidates x 8 heads of 4 bits: 690 us (5.3 ns a tile over the GPU; the exponentials
+// alone 240 us); 64 x 480 x 1024 x 16 heads of 8 bits: 354 us.
 //
 // Design: two blocks an SM, each one stream of items (a user, a head, 128 candidates, a range of
 // the history), 14 warps:

@@ -386,6 +386,9 @@ int genrank_qcache_read(int B, int64_t T, const int32_t *dst_offsets, const int3
  *   cache, R, rows [B] int64, cache_len [B] int32: user u's history is cache rows
  *                [rows[u], rows[u] + cache_len[u]); users in any order, also repeated
  *   max_len      an upper bound of cache_len[u] (host value, at most 2^30)
+ *                max_cand and max_len also choose how the work is cut: from max_cand = 41 on, with
+ *                rows enough, into tiles of 128 candidates, which take as long for a user with few.
+ *                Bounds far above what most users have cost time, and give other last bits
  *   ws, ws_bytes at least genrank_attn_qcached_workspace_size(...) bytes (which may be 0:
  *                then ws may be NULL); contents on entry do not matter
  * Rows of o and lse beyond cand_offsets[B] are left alone.  Device-detected:
