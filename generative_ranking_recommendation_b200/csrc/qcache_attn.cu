@@ -744,8 +744,8 @@ int launch_attn_fwd_qcached(const QcachedAttnArgs& c, cudaStream_t st) {
   // history's time at the end, about 10 ns a row of the bound; what it costs are the blocks that have
   // nothing to do in a pass, 3 ns each, whatever the bound: hence blocks against rows.  Once and twice
   // (us): 1500 blocks of up to 2000 rows 126, 112; 1000 of 2000 202, 191; 3000 of 4000 266, 246; 500 of
-  // 2000 115, 115; beyond the rule 1000 of 480 73, 73, 2000 of
-  // 480 112, 116, 2000 of 1000 195, 193, 3000 of 2000 181, 174.  Histories of one length take the same time either way.
+  // 2000 115, 115.  Where the rule says once: 1000 of 480 73, 73; 2000 of 480 112, 116; 2000 of 1000 195,
+  // 193; 3000 of 2000 181, 174.  Histories of one length take the same time either way.
   P.first = (unsigned)(p.units * p.splits);
   const bool twice = !p.tc && p.splits == 1 && p.units > 444 && p.units < c.max_len;
   const unsigned blocks = twice ? 2 * P.first : P.first;
